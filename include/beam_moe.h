@@ -330,6 +330,48 @@ BEAM_MOE_API beam_moe_status beam_moe_quantize_nvfp4(const float* src, int64_t r
 BEAM_MOE_API beam_moe_status beam_moe_quantize_mxfp8(const float* src, int64_t rows, int64_t cols, uint8_t* codes,
                                                      uint8_t* sf, void* stream);
 
+/* ---- Operators on caller buffers: matrix products grouped by expert with ragged sizes.
+ *
+ * For experts that are not quantised (the recipe's BF16 checkpoint, section "Variants") and for
+ * training them: rows sorted by expert, offsets[e] .. offsets[e + 1] the rows of expert e
+ * (device int32, groups + 1 of them; beam_moe_route's ids, sorted, give them), and
+ *   beam_moe_grouped_gemm         y[r]  = w[e] x[r]
+ *   beam_moe_grouped_gemm_dgrad   dx[r] = w[e]^T dy[r]
+ *   beam_moe_grouped_gemm_wgrad   dw[e] = sum over the rows r of e of dy[r] x[r]^T
+ * with FP32 accumulation on the tensor cores and one rounding to the output's type.  Fused
+ * gate and up projections are one product with n = 2I.
+ *   - x [rows][k], dy [rows][n] and w [groups][n][k] (contiguous) of `type` BEAM_MOE_BF16 or
+ *     BEAM_MOE_FP16; y, dx and dw [groups][n][k] (contiguous) of out_type: `type` or
+ *     BEAM_MOE_FP32.  ld* are the elements from one row to the next: at least the row's
+ *     length, a multiple of 8.  Tensors start on 16-byte boundaries and do not overlap the
+ *     output.
+ *   - n and k are multiples of 8, 1 <= groups <= 1024, rows < 2^31 - 2^16 (else UNSUPPORTED).
+ *     An expert may have no rows: its dw is zero.  rows == 0 enqueues nothing (wgrad: zeroes).
+ *   - offsets are only read on the device: they may come from the kernel before, and a
+ *     captured graph follows them.  They are read as their running maximum clamped to
+ *     [0, rows], so that bad ones give wrong rows but no access outside the buffers.  Rows of y
+ *     and dx before offsets[0] and from offsets[groups] on are left as they were.
+ *   - The tensor cores' FP32 accumulation truncates: a long sum loses about 1e-9 of its
+ *     magnitude per term (5e-6 relative over 4096 terms), which only FP32 outputs show.
+ *   - No workspace, no state: calls on different streams may overlap.
+ * The device side waits are bounded (2 s); beam_moe_check_operators reports one that gave up. */
+enum { BEAM_MOE_BF16 = 0, BEAM_MOE_FP16 = 1, BEAM_MOE_FP32 = 2 };
+BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w, const int32_t* offsets,
+                                                   int32_t rows, int32_t groups, int32_t n, int32_t k, int32_t type,
+                                                   void* y, int64_t ldy, int32_t out_type, void* stream);
+BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const void* w,
+                                                         const int32_t* offsets, int32_t rows, int32_t groups,
+                                                         int32_t n, int32_t k, int32_t type, void* dx, int64_t lddx,
+                                                         int32_t out_type, void* stream);
+BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                                         const int32_t* offsets, int32_t rows, int32_t groups,
+                                                         int32_t n, int32_t k, int32_t type, void* dw,
+                                                         int32_t out_type, void* stream);
+
+/* Synchronises `stream`, then reads and clears the current device's error word of the
+ * operators above (they have no handle).  Returns OK or TIMEOUT. */
+BEAM_MOE_API beam_moe_status beam_moe_check_operators(void* stream);
+
 /* Internal buffers of the last forward, for tests (layouts in the comment of each id). */
 typedef enum {
   BEAM_MOE_BUF_LOGITS = 0,   /* [S][T][E] FP32 partial sums over S slices of H (S = size/(4TE)) */

@@ -30,11 +30,14 @@ EXPORTED = [
     "beam_moe_forward_tp", "beam_moe_forward_tp_phase", "beam_moe_ipc_export", "beam_moe_ipc_import",
     "beam_moe_ipc_close", "beam_moe_create_ep", "beam_moe_create_ep_mxfp8", "beam_moe_forward_ep",
     "beam_moe_forward_ep_phase", "beam_moe_set_router_mode", "beam_moe_set_tp_two_shot_tokens",
-    "beam_moe_set_host_chunk_tokens",
+    "beam_moe_set_host_chunk_tokens", "beam_moe_grouped_gemm", "beam_moe_grouped_gemm_dgrad",
+    "beam_moe_grouped_gemm_wgrad", "beam_moe_check_operators",
 ]
 IPC_HANDLE_BYTES = 64
 FMT_NVFP4, FMT_MXFP8 = 0, 1
 FORMATS = {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8}
+TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
+TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
 
 
 class BeamMoeConfig(ctypes.Structure):
@@ -104,6 +107,10 @@ def _load():
                                            i32, vp, ctypes.POINTER(vp)]),
         "beam_moe_forward_ep": (i32, [vp, vp, vp, vp, i32, vp]),
         "beam_moe_forward_ep_phase": (i32, [vp, vp, vp, vp, i32, i32, vp]),
+        "beam_moe_grouped_gemm": (i32, [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, i32, vp]),
+        "beam_moe_grouped_gemm_dgrad": (i32, [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, i32, vp]),
+        "beam_moe_grouped_gemm_wgrad": (i32, [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, i32, vp]),
+        "beam_moe_check_operators": (i32, [vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -327,6 +334,107 @@ def beam_moe_profile_read(h):
     n = ctypes.c_int32(0)
     _check(_lib.beam_moe_profile_read(h, buf, 32, ctypes.byref(n)), "beam_moe_profile_read")
     return [(_lib.beam_moe_kernel_name(h, i).decode(), float(buf[i])) for i in range(n.value)]
+
+
+# ------------------------------------------------------------------ operators on tensors
+def _on_one_device(*tensors):
+    """The CUDA device of all the tensors given (None stands for one that was not)."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"the tensors have to be on one CUDA device, got {sorted(map(str, devices))}")
+    return next(iter(devices))
+
+
+def _call(name, device, *args, stream=None):
+    """Calls an entry point with `device` current, on `stream` or on that device's current one."""
+    with torch.cuda.device(device):
+        _check(getattr(_lib, name)(*args, _stream(stream)), name)
+
+
+def _row_stride(t, what):
+    """Elements from one row of a 2-D tensor to the next."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} has to be 2-D with its columns next to one another")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _grouped(offsets, *typed):
+    kind = typed[0].dtype
+    if kind not in (torch.bfloat16, torch.float16) or any(t.dtype != kind for t in typed):
+        raise ValueError("the operands have to be both BF16 or both FP16")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets has to be a contiguous int32 vector of groups + 1 row numbers")
+    return kind
+
+
+def _output(out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype not in TYPES:
+        raise ValueError(f"out has to be a BF16, FP16 or FP32 tensor of shape {tuple(shape)}")
+    return out
+
+
+def _expert_weights(w, offsets):
+    if w.dim() != 3 or not w.is_contiguous() or w.shape[0] != offsets.shape[0] - 1:
+        raise ValueError("w has to be a contiguous [groups, n, k] tensor, one matrix for each group of offsets")
+    return w.shape
+
+
+def beam_moe_grouped_gemm(x, w, offsets, out=None, out_dtype=None, stream=None):
+    """y[r] = w[e] x[r] for the rows r of each expert e, offsets[e] <= r < offsets[e + 1].
+
+    x [rows, k] and w [groups, n, k] BF16 or FP16, offsets int32 [groups + 1], all on one device;
+    y [rows, n] in x's type or FP32 (out_dtype, or out's).  Rows of no expert are not written."""
+    kind = _grouped(offsets, x, w)
+    groups, n, k = _expert_weights(w, offsets)
+    ldx = _row_stride(x, "x")
+    if x.shape[1] != k:
+        raise ValueError(f"x has {x.shape[1]} columns and w {k}")
+    y = _output(out, (x.shape[0], n), out_dtype or kind, x.device)
+    _call("beam_moe_grouped_gemm", _on_one_device(x, w, offsets, y), _ptr(x), ldx, _ptr(w), _ptr(offsets), x.shape[0],
+          groups, n, k, TYPES[kind], _ptr(y), _row_stride(y, "out"), TYPES[y.dtype], stream=stream)
+    return y
+
+
+def beam_moe_grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
+    """dx[r] = w[e]^T dy[r]: the gradient of beam_moe_grouped_gemm's x from that of its y.
+
+    dy [rows, n] and w [groups, n, k]; dx [rows, k] in dy's type or FP32.  Rows of no expert are
+    not written."""
+    kind = _grouped(offsets, dy, w)
+    groups, n, k = _expert_weights(w, offsets)
+    lddy = _row_stride(dy, "dy")
+    if dy.shape[1] != n:
+        raise ValueError(f"dy has {dy.shape[1]} columns and w {n} rows")
+    dx = _output(out, (dy.shape[0], k), out_dtype or kind, dy.device)
+    _call("beam_moe_grouped_gemm_dgrad", _on_one_device(dy, w, offsets, dx), _ptr(dy), lddy, _ptr(w), _ptr(offsets),
+          dy.shape[0], groups, n, k, TYPES[kind], _ptr(dx), _row_stride(dx, "out"), TYPES[dx.dtype], stream=stream)
+    return dx
+
+
+def beam_moe_grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, stream=None):
+    """dw[e] = sum over e's rows of dy[r] x[r]^T: the gradient of beam_moe_grouped_gemm's w.
+
+    dy [rows, n] and x [rows, k]; dw [groups, n, k], contiguous, in their type or FP32 (every
+    expert's is written; zero for one without rows)."""
+    kind = _grouped(offsets, dy, x)
+    lddy, ldx = _row_stride(dy, "dy"), _row_stride(x, "x")
+    if dy.shape[0] != x.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows and x {x.shape[0]}")
+    groups, n, k = offsets.shape[0] - 1, dy.shape[1], x.shape[1]
+    dw = _output(out, (groups, n, k), out_dtype or kind, dy.device)
+    if not dw.is_contiguous():
+        raise ValueError("out has to be contiguous")
+    _call("beam_moe_grouped_gemm_wgrad", _on_one_device(dy, x, offsets, dw), _ptr(dy), lddy, _ptr(x), ldx,
+          _ptr(offsets), dy.shape[0], groups, n, k, TYPES[kind], _ptr(dw), TYPES[dw.dtype], stream=stream)
+    return dw
+
+
+def beam_moe_check_operators(device=None, stream=None):
+    """Waits for `stream` and raises if an operator on `device` gave up a wait since the last check."""
+    with torch.cuda.device(device):
+        _check(_lib.beam_moe_check_operators(_stream(stream)), "beam_moe_check_operators")
 
 
 # ------------------------------------------------------------------ handle wrapper

@@ -174,6 +174,8 @@ size_t act_bytes(const beam_moe_ctx* h, int K) {
 
 }  // namespace
 
+void* beam::tensor_map_encode_fn() { return reinterpret_cast<void*>(tensor_map_encoder()); }
+
 extern "C" {
 
 const char* beam_moe_status_string(beam_moe_status s) {
@@ -994,6 +996,13 @@ beam_moe_status beam_moe_debug_copy(beam_moe_t h, int32_t which, void* dst, size
   if (!dst || bytes == 0 || n == 0) return BEAM_MOE_OK;
   BEAM_TRY(cudaMemcpyAsync(dst, src, std::min(bytes, n), cudaMemcpyDeviceToDevice, static_cast<cudaStream_t>(stream)));
   return BEAM_MOE_OK;
+}
+
+beam_moe_status beam_moe_check_operators(void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t bits = 0;
+  BEAM_TRY(take_grouped_gemm_errors(&bits, s));
+  return bits ? BEAM_MOE_ERR_TIMEOUT : BEAM_MOE_OK;
 }
 
 beam_moe_status beam_moe_check(beam_moe_t h, void* stream) {
