@@ -28,12 +28,18 @@ __device__ __forceinline__ uint32_t map_to_cta(const void* p, uint32_t rank) {
   return r;
 }
 
-// Arrivals at a barrier of either CTA (address from map_to_cta).
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+// Arrivals at a barrier of either CTA (address from map_to_cta).  The relaxed ones order no
+// memory accesses of this thread: right where what they announce is a TMA copy (its bytes order
+// themselves) or finished TMEM reads.  A release at cluster scope waits for the thread's
+// outstanding accesses; taken for every stage it cost ~1200 cycles per stage.
+__device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+__device__ __forceinline__ void mbar_arrive_relaxed_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_relaxed_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {

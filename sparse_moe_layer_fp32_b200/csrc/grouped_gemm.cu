@@ -254,13 +254,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
           const int step = i * GG_BK;
           // a ragged stage lands on this CTA's own barrier; warp 2 hands it on
           const bool ragged = MODE == kWgrad && ((end - begin - step) & 15) != 0 && end - begin - step < GG_BK;
-          uint32_t bar;
-          if (ragged) {
-            bar = map_to_cta(&tail->landed[stage], rank);
-          } else {
-            bar = map_to_cta(&tail->full[stage], 0);
-          }
-          mbar_arrive_expect_tx_at(bar, bytes);
+          const uint32_t bar = ragged ? map_to_cta(&tail->landed[stage], rank) : map_to_cta(&tail->full[stage], 0);
+          mbar_arrive_expect_tx_relaxed_at(bar, bytes);
           if (MODE == kFwd) {
             tma_load_3d_pair(sa, &map_a, bar, step, m0, t.group);
           } else if (MODE == kDgrad) {
@@ -300,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       for (int id = first_tile; id < total && ok; id += tile_stride) {
         const GroupedTile t = grouped_tile<MODE>(args, tail, id);
         if (t.steps == 0) continue;
-        if (!mbar_wait_cluster(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag)) {
+        if (!mbar_wait_bounded(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -309,7 +304,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         const uint32_t d = tmem + acc * GG_TILE;
         const int length = MODE == kWgrad ? tail->begin[t.group + 1] - tail->begin[t.group] : args.kdim;
         for (int i = 0; i < t.steps; ++i) {
-          if (!mbar_wait_cluster(&tail->full[stage], phase, abort_flag)) {
+          // a ragged stage was zeroed by a warp of each CTA: acquire those stores
+          const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
+          if (!(ragged ? mbar_wait_cluster(&tail->full[stage], phase, abort_flag)
+                       : mbar_wait_bounded(&tail->full[stage], phase, abort_flag))) {
             ok = false;
             break;
           }
@@ -368,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->full[last], 0));
+        if (lane == 0) mbar_arrive_release_at(map_to_cta(&tail->full[last], 0));
       }
     }
   } else if (warp >= GG_FIRST_EPI) {
@@ -442,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty[acc], 0));
+        if (lane == 0) mbar_arrive_relaxed_at(map_to_cta(&tail->acc_empty[acc], 0));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
