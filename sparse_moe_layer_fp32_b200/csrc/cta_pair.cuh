@@ -53,15 +53,22 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
       : "memory");
   return ok != 0;
 }
-// mbar_wait_bounded at cluster scope: for barriers that the other CTA arrives at.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+// Bounded waits (kWaitLimitNs): false, with *abort_flag set, once the wait ran past the limit or
+// another role gave up.  The clock is first read after kQuietTries tries (each suspends the
+// thread for a while): reading %globaltimer takes about a microsecond, which on every wait that
+// did not succeed at once held a ring stage to ~800 cycles.  kCluster: for barriers that follow
+// plain stores of the other CTA.
+constexpr uint32_t kQuietTries = 256;
+template <bool kCluster = false>
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 0) {
+    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (i % kQuietTries == 0) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
         *abort_flag = 1;
         return false;
       }

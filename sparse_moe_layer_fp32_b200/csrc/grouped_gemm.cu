@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 template <int MODE, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
     grouped_gemm_kernel(const GroupedArgs args, const __grid_constant__ CUtensorMap map_a,
-                        const __grid_constant__ CUtensorMap map_b) {
+                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_b128) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   GroupedTail* tail = reinterpret_cast<GroupedTail*>(smem + GG_STAGES * GG_STAGE);
@@ -245,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         const int begin = MODE == kWgrad ? tail->begin[t.group] : 0;
         const int end = MODE == kWgrad ? tail->begin[t.group + 1] : 0;
         for (int i = 0; i < t.steps; ++i) {
-          if (!mbar_wait_bounded(&tail->empty[stage], phase ^ 1, abort_flag)) {
+          if (!pair_wait(&tail->empty[stage], phase ^ 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -265,7 +265,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             tma_load_2d_pair(sa, &map_a, bar, m0, begin + step);
             tma_load_2d_pair(sa + GG_CHUNK, &map_a, bar, m0 + 64, begin + step);
           }
-          for (int b = 0; b < b_boxes; ++b) {
+          if (MODE != kWgrad && half == 128) {
+            tma_load_2d_pair(sb, &map_b128, bar, step, n0);
+          } else for (int b = 0; b < b_boxes; ++b) {
             if (MODE == kWgrad)
               tma_load_2d_pair(sb + b * GG_CHUNK, &map_b, bar, n0 + b * 64, begin + step);
             else
@@ -295,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       for (int id = first_tile; id < total && ok; id += tile_stride) {
         const GroupedTile t = grouped_tile<MODE>(args, tail, id);
         if (t.steps == 0) continue;
-        if (!mbar_wait_bounded(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag)) {
+        if (!pair_wait(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -306,8 +308,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         for (int i = 0; i < t.steps; ++i) {
           // a ragged stage was zeroed by a warp of each CTA: acquire those stores
           const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
-          if (!(ragged ? mbar_wait_cluster(&tail->full[stage], phase, abort_flag)
-                       : mbar_wait_bounded(&tail->full[stage], phase, abort_flag))) {
+          if (!(ragged ? pair_wait<true>(&tail->full[stage], phase, abort_flag)
+                       : pair_wait(&tail->full[stage], phase, abort_flag))) {
             ok = false;
             break;
           }
@@ -353,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         stage = (stage + t.steps) % GG_STAGES;
         const int rows = tail->begin[t.group + 1] - tail->begin[t.group] - (t.steps - 1) * GG_BK;
         if ((rows & 15) == 0) continue;
-        ok = mbar_wait_bounded(&tail->landed[last], (parity >> last) & 1u, abort_flag);
+        ok = pair_wait(&tail->landed[last], (parity >> last) & 1u, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         parity ^= 1u << last;
@@ -380,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       const GroupedTile t = grouped_tile<MODE>(args, tail, id);
       const bool any = t.steps > 0;
       if (any) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail->acc_full[acc], acc_phase, abort_flag))) break;
+        if (!__all_sync(0xffffffffu, pair_wait(&tail->acc_full[acc], acc_phase, abort_flag))) break;
         tc_fence_after();
       }
       const int m = t.m0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
@@ -471,7 +473,7 @@ bool make_map(CUtensorMap* m, int bf16, const void* base, int dims, uint64_t d0,
 }
 
 template <int MODE, int OUT>
-cudaError_t launch_mode(const GroupedArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, int64_t most_tiles,
+cudaError_t launch_mode(const GroupedArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb2, int64_t most_tiles,
                         cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -482,15 +484,15 @@ cudaError_t launch_mode(const GroupedArgs& a, const CUtensorMap& ma, const CUten
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most_tiles));
   return launch_pdl(grouped_gemm_kernel<MODE, OUT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(GG_THREADS),
-                    kGroupedSmem, s, a, ma, mb);
+                    kGroupedSmem, s, a, ma, mb, mb2);
 }
 
 template <int MODE>
-cudaError_t launch_out(int out_type, const GroupedArgs& a, const CUtensorMap& ma, const CUtensorMap& mb,
+cudaError_t launch_out(int out_type, const GroupedArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb2,
                        int64_t most_tiles, cudaStream_t s) {
-  if (out_type == kTypeBf16) return launch_mode<MODE, kTypeBf16>(a, ma, mb, most_tiles, s);
-  if (out_type == kTypeFp16) return launch_mode<MODE, kTypeFp16>(a, ma, mb, most_tiles, s);
-  return launch_mode<MODE, kTypeFp32>(a, ma, mb, most_tiles, s);
+  if (out_type == kTypeBf16) return launch_mode<MODE, kTypeBf16>(a, ma, mb, mb2, most_tiles, s);
+  if (out_type == kTypeFp16) return launch_mode<MODE, kTypeFp16>(a, ma, mb, mb2, most_tiles, s);
+  return launch_mode<MODE, kTypeFp32>(a, ma, mb, mb2, most_tiles, s);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -506,7 +508,7 @@ cudaError_t launch_grouped_gemm(int mode, const void* rows_a, int64_t ld_a, cons
                                 const void* w, const int32_t* offsets, int64_t rows, int groups, int n, int k,
                                 int in_type, void* out, int64_t ldo, int out_type, cudaStream_t s) {
   const int bf16 = in_type == kTypeBf16;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mb2;
   bool ok;
   GroupedArgs a{offsets, groups, static_cast<int>(rows), mode == kDgrad ? k : n, mode == kDgrad ? n : k, k, out, ldo,
                 bf16};
@@ -514,15 +516,17 @@ cudaError_t launch_grouped_gemm(int mode, const void* rows_a, int64_t ld_a, cons
   if (mode == kWgrad) {
     ok = make_map(&ma, bf16, rows_b, 2, n, rows, 1, ld_b * 2, 0, 64, 64) &&
          make_map(&mb, bf16, rows_a, 2, k, rows, 1, ld_a * 2, 0, 64, 64);
+    mb2 = mb;
   } else {
     ok = make_map(&ma, bf16, w, 3, k, n, groups, row_w, mat_w, 64, mode == kFwd ? 128 : 64) &&
-         make_map(&mb, bf16, rows_a, 2, mode == kFwd ? k : n, rows, 1, ld_a * 2, 0, 64, GG_BOX_ROWS);
+         make_map(&mb, bf16, rows_a, 2, mode == kFwd ? k : n, rows, 1, ld_a * 2, 0, 64, GG_BOX_ROWS) &&
+         make_map(&mb2, bf16, rows_a, 2, mode == kFwd ? k : n, rows, 1, ld_a * 2, 0, 64, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = grouped_gemm_most_tiles(mode, rows, groups, n, k);
-  if (mode == kFwd) return launch_out<kFwd>(out_type, a, ma, mb, tiles, s);
-  if (mode == kDgrad) return launch_out<kDgrad>(out_type, a, ma, mb, tiles, s);
-  return launch_out<kWgrad>(out_type, a, ma, mb, tiles, s);
+  if (mode == kFwd) return launch_out<kFwd>(out_type, a, ma, mb, mb2, tiles, s);
+  if (mode == kDgrad) return launch_out<kDgrad>(out_type, a, ma, mb, mb2, tiles, s);
+  return launch_out<kWgrad>(out_type, a, ma, mb, mb2, tiles, s);
 }
 
 cudaError_t take_grouped_gemm_errors(uint32_t* bits, cudaStream_t s) {
