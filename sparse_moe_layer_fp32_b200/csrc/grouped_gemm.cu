@@ -159,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   GroupedTail* tail = reinterpret_cast<GroupedTail*>(smem + GG_STAGES * GG_STAGE);
   volatile int* abort_flag = &tail->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
 
   if (threadIdx.x == 0) {
@@ -231,29 +231,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int id = first_tile; id < total && ok; id += tile_stride) {
-        const GroupedTile t = grouped_tile<MODE>(args, tail, id);
-        const int half = t.n >> 1;
-        const int b_boxes = MODE == kWgrad ? (half + 63) / 64 : (half + GG_BOX_ROWS - 1) / GG_BOX_ROWS;
-        const uint32_t bytes =
-            GG_OPERAND + static_cast<uint32_t>(b_boxes) * (MODE == kWgrad ? GG_CHUNK : GG_BOX_ROWS * 128);
-        const int m0 = t.m0 + static_cast<int>(rank) * 128, n0 = t.n0 + static_cast<int>(rank) * half;
-        const int begin = MODE == kWgrad ? tail->begin[t.group] : 0;
-        const int end = MODE == kWgrad ? tail->begin[t.group + 1] : 0;
-        for (int i = 0; i < t.steps; ++i) {
-          if (!pair_wait(&tail->empty[stage], phase ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * GG_STAGE;
-          uint8_t* sb = sa + GG_OPERAND;
-          const int step = i * GG_BK;
-          // a ragged stage lands on this CTA's own barrier; warp 2 hands it on
-          const bool ragged = MODE == kWgrad && ((end - begin - step) & 15) != 0 && end - begin - step < GG_BK;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int id = first_tile; id < total && ok; id += tile_stride) {
+      const GroupedTile t = grouped_tile<MODE>(args, tail, id);
+      const int half = t.n >> 1;
+      const int b_boxes = MODE == kWgrad ? (half + 63) / 64 : (half + GG_BOX_ROWS - 1) / GG_BOX_ROWS;
+      const uint32_t bytes = GG_OPERAND + static_cast<uint32_t>(b_boxes) * (MODE == kWgrad ? GG_CHUNK : GG_BOX_ROWS * 128);
+      const int m0 = t.m0 + static_cast<int>(rank) * 128, n0 = t.n0 + static_cast<int>(rank) * half;
+      const int begin = MODE == kWgrad ? tail->begin[t.group] : 0;
+      const int length = MODE == kWgrad ? tail->begin[t.group + 1] - begin : 0;
+      for (int i = 0; i < t.steps; ++i) {
+        ok = __all_sync(0xffffffffu, pair_wait(&tail->empty[stage], phase ^ 1, abort_flag));
+        if (!ok) break;
+        uint8_t* sa = smem + stage * GG_STAGE;
+        uint8_t* sb = sa + GG_OPERAND;
+        const int step = i * GG_BK;
+        // a ragged stage lands on this CTA's own barrier; warp 2 hands it on
+        const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
+        if (elect_one()) {
           const uint32_t bar = ragged ? map_to_cta(&tail->landed[stage], rank) : map_to_cta(&tail->full[stage], 0);
           mbar_arrive_expect_tx_relaxed_at(bar, bytes);
           if (MODE == kFwd) {
@@ -265,28 +262,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             tma_load_2d_pair(sa, &map_a, bar, m0, begin + step);
             tma_load_2d_pair(sa + GG_CHUNK, &map_a, bar, m0 + 64, begin + step);
           }
-          if (MODE != kWgrad && half == 128) {
+          if (MODE == kWgrad) {
+            tma_load_2d_pair(sb, &map_b, bar, n0, begin + step);
+            if (b_boxes == 2) tma_load_2d_pair(sb + GG_CHUNK, &map_b, bar, n0 + 64, begin + step);
+          } else if (half == 128) {
             tma_load_2d_pair(sb, &map_b128, bar, step, n0);
-          } else for (int b = 0; b < b_boxes; ++b) {
-            if (MODE == kWgrad)
-              tma_load_2d_pair(sb + b * GG_CHUNK, &map_b, bar, n0 + b * 64, begin + step);
-            else
+          } else {
+            for (int b = 0; b < b_boxes; ++b)
               tma_load_2d_pair(sb + b * GG_BOX_ROWS * 128, &map_b, bar, step, n0 + b * GG_BOX_ROWS);
           }
-          if (++stage == GG_STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++stage == GG_STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (!ok) {  // the copies still in flight land long before this
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
-      }
+    }
+    if (!ok) {  // the copies still in flight land long before this
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -294,13 +293,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       // FP32 accumulator, operand types, M- and N-major operands, M = 256
       const uint32_t idesc0 = (1u << 4) | (type << 7) | (type << 10) | ((MODE != kFwd ? 1u : 0u) << 15) |
                               ((MODE == kWgrad ? 1u : 0u) << 16) | ((GG_TILE >> 4) << 24);
+      // Descriptors of stage 0; their low words hold the address in units of 16 bytes.  16
+      // reduction steps further: 32 bytes of each line, or 16 lines of each chunk.
+      constexpr uint32_t kStepA = MODE == kFwd ? 32 / 16 : 2048 / 16, kStepB = MODE == kWgrad ? 2048 / 16 : 32 / 16;
+      const uint32_t base = smem_u32(smem);
+      const uint64_t da0 = MODE == kFwd ? sdesc_k_sw128(base) : sdesc_mn_sw128(base, GG_CHUNK);
+      const uint64_t db0 =
+          MODE == kWgrad ? sdesc_mn_sw128(base + GG_OPERAND, GG_CHUNK) : sdesc_k_sw128(base + GG_OPERAND);
       for (int id = first_tile; id < total && ok; id += tile_stride) {
         const GroupedTile t = grouped_tile<MODE>(args, tail, id);
         if (t.steps == 0) continue;
-        if (!pair_wait(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_empty[acc], acc_phase ^ 1, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n >> 3) << 17);
         const uint32_t d = tmem + acc * GG_TILE;
@@ -308,20 +312,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         for (int i = 0; i < t.steps; ++i) {
           // a ragged stage was zeroed by a warp of each CTA: acquire those stores
           const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
-          if (!(ragged ? pair_wait<true>(&tail->full[stage], phase, abort_flag)
-                       : pair_wait(&tail->full[stage], phase, abort_flag))) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, ragged ? pair_wait<true>(&tail->full[stage], phase, abort_flag)
+                                              : pair_wait(&tail->full[stage], phase, abort_flag));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * GG_STAGE), sb = sa + GG_OPERAND;
-          const int count = min(GG_BK / 16, (length - i * GG_BK + 15) >> 4);
-          for (int j = 0; j < count; ++j) {
-            // 16 reduction steps: 32 bytes of each line, or 16 lines of each chunk
-            const uint64_t da = MODE == kFwd ? sdesc_k_sw128(sa + j * 32) : sdesc_mn_sw128(sa + j * 2048, GG_CHUNK);
-            const uint64_t db = MODE == kWgrad ? sdesc_mn_sw128(sb + j * 2048, GG_CHUNK) : sdesc_k_sw128(sb + j * 32);
-            tc_mma_f16_pair(d, da, db, idesc, (i | j) != 0 ? 1u : 0u);
-          }
+          const uint64_t da = da0 + static_cast<uint64_t>(stage * (GG_STAGE / 16));
+          const uint64_t db = db0 + static_cast<uint64_t>(stage * (GG_STAGE / 16));
+          const int left = length - i * GG_BK;
+#pragma unroll
+          for (int j = 0; j < GG_BK / 16; ++j)
+            if (j * 16 < left) tc_mma_f16_pair(d, da + j * kStepA, db + j * kStepB, idesc, (i | j) != 0 ? 1u : 0u);
           tc_commit_pair(&tail->empty[stage]);
           if (++stage == GG_STAGES) {
             stage = 0;
