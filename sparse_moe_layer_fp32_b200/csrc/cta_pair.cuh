@@ -108,13 +108,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 // Arrives once on `bar` of both CTAs when every MMA issued before (by the lane that the converged
 // warp elects, always the same one) has completed.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3)), "r"(leader)
       : "memory");
 }
 // One lane of a converged warp.  The roles that issue TMA copies and MMAs run as whole warps and
@@ -132,13 +132,13 @@ __device__ __forceinline__ bool elect_one() {
 // D(tmem) (+)= A(smem) * B(smem)^T over the pair, BF16 or FP16 operands, FP32 accumulation;
 // issued by one lane of the converged warp.
 __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
+                                                uint32_t accumulate, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 

@@ -289,6 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint32_t leader = elect_one() ? 1u : 0u;
       const uint32_t type = args.bf16 ? 1u : 0u;
       // FP32 accumulator, operand types, M- and N-major operands, M = 256
       const uint32_t idesc0 = (1u << 4) | (type << 7) | (type << 10) | ((MODE != kFwd ? 1u : 0u) << 15) |
@@ -321,22 +322,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
           const int left = length - i * GG_BK;
 #pragma unroll
           for (int j = 0; j < GG_BK / 16; ++j)
-            if (j * 16 < left) tc_mma_f16_pair(d, da + j * kStepA, db + j * kStepB, idesc, (i | j) != 0 ? 1u : 0u);
-          tc_commit_pair(&tail->empty[stage]);
+            if (j * 16 < left) tc_mma_f16_pair(d, da + j * kStepA, db + j * kStepB, idesc, (i | j) != 0 ? 1u : 0u, leader);
+          tc_commit_pair(&tail->empty[stage], leader);
           if (++stage == GG_STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        tc_commit_pair(&tail->acc_full[acc]);
+        tc_commit_pair(&tail->acc_full[acc], leader);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
         }
       }
       if (!ok) {  // nothing may read shared memory or write TMEM after the CTAs are gone
-        tc_commit_pair(&tail->drain);
+        tc_commit_pair(&tail->drain, leader);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&tail->drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
