@@ -288,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
     if (rank == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       const uint32_t leader = elect_one() ? 1u : 0u;
       const uint32_t type = args.bf16 ? 1u : 0u;
       // FP32 accumulator, operand types, M- and N-major operands, M = 256
@@ -313,10 +313,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         for (int i = 0; i < t.steps; ++i) {
           // a ragged stage was zeroed by a warp of each CTA: acquire those stores
           const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
-          ok = __all_sync(0xffffffffu, ragged ? pair_wait<true>(&tail->full[stage], phase, abort_flag)
-                                              : pair_wait(&tail->full[stage], phase, abort_flag));
-          if (!ok) break;
+          if (!ready || ragged) {
+            ok = __all_sync(0xffffffffu, ragged ? pair_wait<true>(&tail->full[stage], phase, abort_flag)
+                                                : pair_wait(&tail->full[stage], phase, abort_flag));
+            if (!ok) break;
+          }
           tc_fence_after();
+          // look at the next stage's barrier while this stage's MMAs go out
+          const int next = stage + 1 == GG_STAGES ? 0 : stage + 1;
+          const uint32_t next_phase = phase ^ (next == 0 ? 1u : 0u);
+          const bool next_ready = mbar_test(&tail->full[next], next_phase);
           const uint64_t da = da0 + static_cast<uint64_t>(stage * (GG_STAGE / 16));
           const uint64_t db = db0 + static_cast<uint64_t>(stage * (GG_STAGE / 16));
           const int left = length - i * GG_BK;
@@ -324,10 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
           for (int j = 0; j < GG_BK / 16; ++j)
             if (j * 16 < left) tc_mma_f16_pair(d, da + j * kStepA, db + j * kStepB, idesc, (i | j) != 0 ? 1u : 0u, leader);
           tc_commit_pair(&tail->empty[stage], leader);
-          if (++stage == GG_STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+          stage = next;
+          phase = next_phase;
+          ready = __all_sync(0xffffffffu, next_ready);
         }
         if (!ok) break;
         tc_commit_pair(&tail->acc_full[acc], leader);
