@@ -368,6 +368,49 @@ BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t
                                                          int32_t n, int32_t k, int32_t type, void* dw,
                                                          int32_t out_type, void* stream);
 
+/* ---- Operators on caller buffers: 4-bit microscaled floating point.
+ *
+ * Formats: E2M1 codes, two to a byte (element 2i in the low nibble), with
+ *   BEAM_MOE_FP4_MX  MXFP4: one UE8M0 byte per 32 consecutive values of a row (an exponent with
+ *                    bias 127), the smallest 2^e, e >= -127, with amax <= 6 * 2^e;
+ *   BEAM_MOE_FP4_NV  NVFP4 as in the rest of this file: one E4M3 byte per 16 values and one FP32
+ *                    tensor scale alpha; the codes of beam_moe_quantize_nvfp4.
+ * A quantised [rows][cols] matrix is codes [rows][cols / 2] and scale bytes
+ * [rows][cols / 32 or cols / 16], both row-major; their rows may be further apart (ldc, ldsf:
+ * bytes from one row to the next, multiples of 16).  What lies between a row's last scale and
+ * the next row is neither written nor used.  cols is a multiple of 32 (else UNSUPPORTED); all
+ * pointers start on 16-byte boundaries, tensor scales on 4-byte ones. */
+enum { BEAM_MOE_FP4_MX = 0, BEAM_MOE_FP4_NV = 1 };
+
+/* src [rows][cols] of src_type (BF16, FP16 or FP32), rows ld elements apart (a multiple of 16
+ * bytes).  alpha and alpha_out as in beam_moe_quantize_nvfp4: alpha > 0 is NVFP4's tensor scale;
+ * alpha <= 0 takes the largest finite |src| / 2688, found on the device.  alpha_out (device
+ * FP32; may be NULL where alpha > 0) receives the scale used.  MXFP4 uses neither.  A block that
+ * holds a NaN or an infinity gets a NaN scale and zero codes: it reads back, and multiplies, as
+ * NaN. */
+BEAM_MOE_API beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t src_type, int64_t ld,
+                                                   int64_t rows, int32_t cols, float alpha, uint8_t* codes,
+                                                   int64_t ldc, uint8_t* sf, int64_t ldsf, float* alpha_out,
+                                                   void* stream);
+/* out [rows][cols] of out_type, rows ldo elements apart (a multiple of 16 bytes): code * scale
+ * (exact), times *alpha (NVFP4; device FP32, NULL = 1) in FP32, rounded once to out_type. */
+BEAM_MOE_API beam_moe_status beam_moe_dequantize_fp4(int32_t format, const uint8_t* codes, int64_t ldc,
+                                                     const uint8_t* sf, int64_t ldsf, const float* alpha,
+                                                     int64_t rows, int32_t cols, void* out, int32_t out_type,
+                                                     int64_t ldo, void* stream);
+/* out[m][n] = alpha_a alpha_b sum_k a[m][k] b[n][k]: a W4A4 projection, a the quantised
+ * activations, b the quantised weights, both of one format, on the block-scaled tensor cores
+ * with FP32 accumulation and one rounding to out_type (BF16, FP16 or FP32).  m and n are any
+ * sizes from 0 on (from 1 token), k a multiple of 32; ldo >= n elements.  alpha_a, alpha_b:
+ * device FP32 tensor scales of NVFP4 operands (NULL = 1; not used for MXFP4).  No workspace;
+ * calls on different streams may overlap.  A wait that gave up is reported by
+ * beam_moe_check_operators. */
+BEAM_MOE_API beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_codes, int64_t lda,
+                                               const uint8_t* a_sf, int64_t lda_sf, const float* alpha_a,
+                                               const uint8_t* b_codes, int64_t ldb, const uint8_t* b_sf,
+                                               int64_t ldb_sf, const float* alpha_b, int32_t m, int32_t n, int32_t k,
+                                               void* out, int32_t out_type, int64_t ldo, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error word of the
  * operators above (they have no handle).  Returns OK or TIMEOUT. */
 BEAM_MOE_API beam_moe_status beam_moe_check_operators(void* stream);

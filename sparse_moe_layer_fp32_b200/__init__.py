@@ -31,12 +31,16 @@ EXPORTED = [
     "beam_moe_ipc_close", "beam_moe_create_ep", "beam_moe_create_ep_mxfp8", "beam_moe_forward_ep",
     "beam_moe_forward_ep_phase", "beam_moe_set_router_mode", "beam_moe_set_tp_two_shot_tokens",
     "beam_moe_set_host_chunk_tokens", "beam_moe_grouped_gemm", "beam_moe_grouped_gemm_dgrad",
-    "beam_moe_grouped_gemm_wgrad", "beam_moe_check_operators",
+    "beam_moe_grouped_gemm_wgrad", "beam_moe_check_operators", "beam_moe_quantize_fp4", "beam_moe_dequantize_fp4",
+    "beam_moe_gemm_fp4",
 ]
 IPC_HANDLE_BYTES = 64
 FMT_NVFP4, FMT_MXFP8 = 0, 1
 FORMATS = {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8}
 TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
+FP4_MX, FP4_NV = 0, 1
+FP4_FORMATS = {"mxfp4": FP4_MX, "nvfp4": FP4_NV}
+FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
 
 
@@ -111,6 +115,9 @@ def _load():
         "beam_moe_grouped_gemm_dgrad": (i32, [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, i32, vp]),
         "beam_moe_grouped_gemm_wgrad": (i32, [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, i32, vp]),
         "beam_moe_check_operators": (i32, [vp]),
+        "beam_moe_quantize_fp4": (i32, [i32, vp, i32, i64, i64, i32, f32, vp, i64, vp, i64, vp, vp]),
+        "beam_moe_dequantize_fp4": (i32, [i32, vp, i64, vp, i64, vp, i64, i32, vp, i32, i64, vp]),
+        "beam_moe_gemm_fp4": (i32, [i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32, i32, vp, i32, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -429,6 +436,94 @@ def beam_moe_grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, stream
     _call("beam_moe_grouped_gemm_wgrad", _on_one_device(dy, x, offsets, dw), _ptr(dy), lddy, _ptr(x), ldx,
           _ptr(offsets), dy.shape[0], groups, n, k, TYPES[kind], _ptr(dw), TYPES[dw.dtype], stream=stream)
     return dw
+
+
+def _fp4_format(fmt):
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"unknown 4-bit format {fmt!r}")
+    return FP4_FORMATS[fmt]
+
+
+def _fp4_matrix(codes, sf, fmt, what):
+    """(rows, cols, bytes between rows of codes, of scales) of a quantised matrix."""
+    if codes.dtype != torch.uint8 or sf.dtype != torch.uint8:
+        raise ValueError(f"{what}'s codes and scales have to be uint8 tensors")
+    rows, cols = codes.shape[0], codes.shape[1] * 2 if codes.dim() == 2 else 0
+    if codes.dim() != 2 or tuple(sf.shape) != (rows, cols // FP4_BLOCK[fmt]):
+        raise ValueError(f"{what} has to be codes [rows, cols / 2] and scales [rows, cols / {FP4_BLOCK[fmt]}]")
+    ldc, ldsf = _row_stride(codes, f"{what}'s codes"), _row_stride(sf, f"{what}'s scales")
+    if rows == 1:  # a single row's pitch is never stepped over: any that the library takes will do
+        ldsf = (max(ldsf, sf.shape[1]) + 15) // 16 * 16
+    return rows, cols, ldc, ldsf
+
+
+def _tensor_scale(alpha, fmt, what):
+    if alpha is None or fmt == "mxfp4":
+        return None
+    if alpha.dtype != torch.float32 or alpha.numel() != 1:
+        raise ValueError(f"{what} has to be one FP32 value on the device")
+    return alpha
+
+
+def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
+    """MXFP4 ("mxfp4") or NVFP4 ("nvfp4") of a 2-D BF16, FP16 or FP32 tensor.
+
+    Returns (codes uint8 [rows, cols / 2], scales uint8 [rows, cols / 32 or 16], alpha): the
+    scales' rows lie a multiple of 16 bytes apart, as beam_moe_gemm_fp4 wants them.  NVFP4:
+    alpha is the tensor scale, a float; None takes the largest finite value / 2688, found on
+    the device.  The alpha returned is an FP32 tensor [1] (None for MXFP4)."""
+    form = _fp4_format(fmt)
+    if src.dtype not in TYPES:
+        raise ValueError("src has to be BF16, FP16 or FP32")
+    ld = _row_stride(src, "src")
+    rows, cols = src.shape
+    blocks = cols // FP4_BLOCK[fmt]
+    device = _on_one_device(src)
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+    sf = torch.empty((rows, (blocks + 15) // 16 * 16), dtype=torch.uint8, device=device)
+    if alpha is not None and not 0.0 < float(alpha) < float("inf"):
+        raise ValueError("alpha has to be a positive finite number")
+    scale = None
+    if fmt == "nvfp4":  # the library writes it; an empty tensor has none
+        scale = (torch.empty if src.numel() else torch.zeros)(1, dtype=torch.float32, device=device)
+    with torch.cuda.device(device):
+        _check(_lib.beam_moe_quantize_fp4(form, _ptr(src), TYPES[src.dtype], ld, rows, cols,
+                                          ctypes.c_float(-1.0 if alpha is None else float(alpha)), _ptr(codes),
+                                          max(cols // 2, 16), _ptr(sf), max(sf.shape[1], 16), _ptr(scale),
+                                          _stream(stream)), "beam_moe_quantize_fp4")
+    return codes, sf[:, :blocks], scale
+
+
+def beam_moe_dequantize_fp4(codes, sf, fmt, alpha=None, out_dtype=torch.bfloat16, stream=None):
+    """The values [rows, cols] of a matrix from beam_moe_quantize_fp4, in out_dtype."""
+    form = _fp4_format(fmt)
+    rows, cols, ldc, ldsf = _fp4_matrix(codes, sf, fmt, "the matrix")
+    alpha = _tensor_scale(alpha, fmt, "alpha")
+    if out_dtype not in TYPES:
+        raise ValueError("out_dtype has to be BF16, FP16 or FP32")
+    device = _on_one_device(codes, sf, alpha)
+    out = torch.empty((rows, cols), dtype=out_dtype, device=device)
+    _call("beam_moe_dequantize_fp4", device, form, _ptr(codes), ldc, _ptr(sf), ldsf, _ptr(alpha), rows, cols,
+          _ptr(out), TYPES[out_dtype], max(cols, 8), stream=stream)
+    return out
+
+
+def beam_moe_gemm_fp4(a_codes, a_sf, b_codes, b_sf, fmt, alpha_a=None, alpha_b=None, out=None, out_dtype=None,
+                      stream=None):
+    """out [m, n] = a [m, k] times b [n, k] transposed, both quantised in fmt, in out_dtype (or
+    out's type; BF16 where neither is given).  alpha_a, alpha_b: NVFP4's tensor scales, FP32
+    tensors [1] on the device (None: 1)."""
+    form = _fp4_format(fmt)
+    m, k, lda, lda_sf = _fp4_matrix(a_codes, a_sf, fmt, "a")
+    n, kb, ldb, ldb_sf = _fp4_matrix(b_codes, b_sf, fmt, "b")
+    if k != kb:
+        raise ValueError(f"a has {k} columns and b {kb}")
+    alpha_a, alpha_b = _tensor_scale(alpha_a, fmt, "alpha_a"), _tensor_scale(alpha_b, fmt, "alpha_b")
+    out = _output(out, (m, n), out_dtype or torch.bfloat16, a_codes.device)
+    _call("beam_moe_gemm_fp4", _on_one_device(a_codes, a_sf, b_codes, b_sf, alpha_a, alpha_b, out), form,
+          _ptr(a_codes), lda, _ptr(a_sf), lda_sf, _ptr(alpha_a), _ptr(b_codes), ldb, _ptr(b_sf), ldb_sf,
+          _ptr(alpha_b), m, n, k, _ptr(out), TYPES[out.dtype], _row_stride(out, "out"), stream=stream)
+    return out
 
 
 def beam_moe_check_operators(device=None, stream=None):

@@ -28,15 +28,16 @@ __device__ __forceinline__ uint32_t map_to_cta(const void* p, uint32_t rank) {
   return r;
 }
 
-// Arrivals at a barrier of either CTA (address from map_to_cta).  The relaxed ones order no
-// memory accesses of this thread: right where what they announce is a TMA copy (its bytes order
-// themselves) or finished TMEM reads.  A release at cluster scope waits for the thread's
-// outstanding accesses; taken for every stage it cost ~1200 cycles per stage.
+// Arrivals at a barrier of either CTA (address from map_to_cta).  Plain: releases this thread's
+// accesses to its own CTA only, which is right where what it announces are finished TMEM
+// accesses.  The relaxed one announces TMA copies (their bytes order themselves).  A release at
+// cluster scope waits for the thread's outstanding accesses; taken for every stage of a ring it
+// cost ~1200 cycles per stage.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_relaxed_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed_at(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)

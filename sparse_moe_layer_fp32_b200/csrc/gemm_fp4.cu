@@ -1,0 +1,485 @@
+// Product of two 4-bit microscaled matrices, D[m][n] = sum_k A[m][k] B[n][k], both MXFP4 or both
+// NVFP4 (codes and scales row-major, as the quantisers leave them), FP32 accumulation, one
+// rounding to BF16, FP16 or FP32: a W4A4 projection with A the activations and B the weights.
+//
+// tcgen05.mma block-scaled over CTA pairs, 256 x 256 tiles; kind::mxf4 (E2M1, one UE8M0 scale
+// per 32) or kind::mxf4nvf4 (E2M1, one E4M3 scale per 16).  The scales multiply inside the
+// MMA; NVFP4's two tensor scales multiply the accumulator.
+//
+// B's rows (the weights' features) are the tensor core's M and A's rows (tokens) its N, which
+// may be any multiple of 32 up to 256: one token costs an N of 32, and the kernel streams weights.
+//
+// Scales.  The tensor core wants them in TMEM: the scales of operand row m at lane m % 32 (in
+// all four lane quarters), column m / 32, 32 bits per row and K group.  Four warps of each CTA
+// read them from the row-major bytes that TMA brought (16 bytes per row and K step) and store
+// them with tcgen05.st, each its lane quarter: a copy on the tensor pipe would wait for
+// the MMAs there.  Each CTA needs the scales of its own 128 M rows and of all N rows.  Bytes
+// past a row's last scale are filled with zeros by TMA, so that what lies behind them in memory
+// (a NaN byte times a zero code would be NaN) does not matter.
+//
+// A CTA (768 threads): warp 0 loads (a ring of 5 stages of 38 KB: 256 K values of 128 B rows
+// and of half of the A rows, and their scales), warp 1 of the leading CTA issues the MMAs, warp
+// 3 owns TMEM, warps 4..7 move scales, warps 8..23 store results.  One accumulator of 256
+// columns (the scales of five stages take the other half of TMEM): the storing warps read it
+// into registers and release it before they convert and store.
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "../../include/beam_moe.h"
+#include "cta_pair.cuh"
+#include "internal.h"
+
+namespace beam {
+
+namespace {
+
+__device__ uint32_t g_fp4_err;  // error bits of this device's 4-bit products
+
+constexpr int F4_BK = 256;                      // K values of a stage: one 128-byte line of codes
+constexpr int F4_STAGES = 5;
+constexpr int F4_CODES = 128 * 128;             // 16 KB: codes of 128 rows
+constexpr int F4_OFF_N = F4_CODES;              // N-side codes
+constexpr int F4_OFF_SFM = 2 * F4_CODES;        // scales of this CTA's 128 M rows
+constexpr int F4_OFF_SFN = F4_OFF_SFM + 128 * 16;
+constexpr int F4_STAGE = F4_OFF_SFN + 256 * 16;
+static_assert(F4_STAGE % 1024 == 0, "swizzled lines start on 1 KB boundaries");
+constexpr int F4_TILE = 256;
+constexpr int F4_BOX = 32;                      // rows of a short load
+constexpr int F4_PANEL = 8;                     // row blocks of A that share B in turn
+constexpr int F4_SF_COL = 256;                  // TMEM columns of the stages' scales
+constexpr int F4_SF_STAGE = 48;                 // M: 4 columns per K group, then N: 8 per K group
+constexpr int F4_SF_N = 16;
+static_assert(F4_SF_COL + F4_STAGES * F4_SF_STAGE <= 512, "scales fit in TMEM");
+constexpr int F4_FIRST_SF = 4, F4_FIRST_EPI = 8, F4_EPI_WARPS = 16;
+constexpr int F4_THREADS = 32 * (F4_FIRST_EPI + F4_EPI_WARPS);
+
+struct Fp4Args {
+  int m, n, k;             // D is [m][n]
+  const float* alpha_a;    // tensor scales, or nullptr
+  const float* alpha_b;
+  void* out;
+  int64_t ldo;
+};
+
+struct __align__(16) Fp4Tail {
+  uint64_t full[F4_STAGES];      // this CTA's operands and scales have landed
+  uint64_t empty[F4_STAGES];
+  uint64_t sf_full[F4_STAGES];   // leader: both CTAs' scales are in TMEM (their operands have landed)
+  uint64_t acc_full;
+  uint64_t acc_empty;            // leader
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kFp4Smem = static_cast<size_t>(F4_STAGES) * F4_STAGE + sizeof(Fp4Tail) + 1024;
+static_assert(kFp4Smem <= 227 * 1024, "shared memory of one CTA");
+
+struct Fp4Tile {
+  int f0;          // first feature (row of B)
+  int r0, r_end;   // rows of A
+  int n;           // their number rounded up to 32
+};
+
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& a, int id) {
+  Fp4Tile t;
+  const int ft = (a.n + F4_TILE - 1) / F4_TILE;
+  const int blocks = (a.m + F4_TILE - 1) / F4_TILE;
+  const int panel = id / (F4_PANEL * ft);
+  const int rest = id - panel * F4_PANEL * ft;
+  const int wide = min(F4_PANEL, blocks - panel * F4_PANEL);
+  t.f0 = rest / wide * F4_TILE;
+  const int block = panel * F4_PANEL + rest % wide;
+  const int height = ((a.m + blocks - 1) / blocks + 31) & ~31;  // equal blocks
+  t.r0 = block * height;
+  t.r_end = min(a.m, t.r0 + height);
+  t.n = max(32, (t.r_end - t.r0 + 31) & ~31);
+  return t;
+}
+
+template <int FORMAT>
+__device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t leader) {
+  if constexpr (FORMAT == BEAM_MOE_FP4_MX)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(leader)
+        : "memory");
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (OUT == kTypeBf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+struct Fp4Maps {
+  CUtensorMap m_codes, n_codes, n_codes32, m_sf, n_sf, n_sf32;
+};
+
+template <int FORMAT, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
+    gemm_fp4_kernel(const Fp4Args args, const __grid_constant__ Fp4Maps maps) {
+  constexpr bool kMx = FORMAT == BEAM_MOE_FP4_MX;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Fp4Tail* tail = reinterpret_cast<Fp4Tail*>(smem + F4_STAGES * F4_STAGE);
+  volatile int* abort_flag = &tail->abort_flag;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&maps.m_codes);
+    prefetch_tmap(&maps.n_codes);
+    prefetch_tmap(&maps.m_sf);
+    prefetch_tmap(&maps.n_sf);
+    for (int i = 0; i < F4_STAGES; ++i) {
+      mbar_init(&tail->full[i], 1);
+      mbar_init(&tail->empty[i], 1);
+      mbar_init(&tail->sf_full[i], 8);
+    }
+    mbar_init(&tail->acc_full, 1);
+    mbar_init(&tail->acc_empty, 2 * F4_EPI_WARPS);
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc_pair(&tail->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are set before anyone arrives at them
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = tail->tmem_base;
+  const int total = ((args.m + F4_TILE - 1) / F4_TILE) * ((args.n + F4_TILE - 1) / F4_TILE);
+  const int first_tile = blockIdx.x >> 1, tile_stride = gridDim.x >> 1;
+  const int steps = (args.k + F4_BK - 1) / F4_BK;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int id = first_tile; id < total && ok; id += tile_stride) {
+      const Fp4Tile t = fp4_tile(args, id);
+      const int half = t.n >> 1;
+      const int f0 = t.f0 + static_cast<int>(rank) * 128, r0 = t.r0 + static_cast<int>(rank) * half;
+      const int code_boxes = (half + F4_BOX - 1) / F4_BOX, sf_boxes = t.n / F4_BOX;
+      const uint32_t bytes = F4_CODES + 128 * 16 + static_cast<uint32_t>(code_boxes) * F4_BOX * 128 +
+                             static_cast<uint32_t>(sf_boxes) * F4_BOX * 16;
+      for (int i = 0; i < steps; ++i) {
+        ok = __all_sync(0xffffffffu, pair_wait(&tail->empty[stage], phase ^ 1, abort_flag));
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* s = smem + stage * F4_STAGE;
+          uint64_t* bar = &tail->full[stage];
+          // 16 scale bytes of a row: this K step's (NVFP4), or those of an even step and the next
+          const int sx = kMx ? (i >> 1) * 16 : i * 16;
+          mbar_arrive_expect_tx(bar, bytes);
+          tma_load_2d(s, &maps.m_codes, bar, i * 128, f0);
+          tma_load_2d(s + F4_OFF_SFM, &maps.m_sf, bar, sx, f0);
+          if (half == 128) {
+            tma_load_2d(s + F4_OFF_N, &maps.n_codes, bar, i * 128, r0);
+            tma_load_2d(s + F4_OFF_SFN, &maps.n_sf, bar, sx, t.r0);
+          } else {
+            for (int b = 0; b < code_boxes; ++b)
+              tma_load_2d(s + F4_OFF_N + b * F4_BOX * 128, &maps.n_codes32, bar, i * 128, r0 + b * F4_BOX);
+            for (int b = 0; b < sf_boxes; ++b)
+              tma_load_2d(s + F4_OFF_SFN + b * F4_BOX * 16, &maps.n_sf32, bar, sx, t.r0 + b * F4_BOX);
+          }
+        }
+        __syncwarp();
+        if (++stage == F4_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // the copies still in flight land long before this
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, ready = false;
+      const uint32_t leader = elect_one() ? 1u : 0u;
+      // E2M1 operands, E4M3 or UE8M0 scales, K-major, M = 256
+      const uint32_t idesc0 = (1u << 7) | (1u << 10) | ((kMx ? 1u : 0u) << 23) | ((F4_TILE >> 4) << 24);
+      const uint64_t da0 = sdesc_k_sw128(smem_u32(smem)), db0 = sdesc_k_sw128(smem_u32(smem) + F4_OFF_N);
+      for (int id = first_tile; id < total && ok; id += tile_stride) {
+        const Fp4Tile t = fp4_tile(args, id);
+        ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_empty, acc_phase ^ 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n >> 3) << 17);
+        for (int i = 0; i < steps; ++i) {
+          if (!ready) {
+            ok = __all_sync(0xffffffffu, pair_wait(&tail->sf_full[stage], phase, abort_flag));
+            if (!ok) break;
+          }
+          tc_fence_after();
+          // look at the next stage's barrier while this stage's MMAs go out
+          const int next = stage + 1 == F4_STAGES ? 0 : stage + 1;
+          const uint32_t next_phase = phase ^ (next == 0 ? 1u : 0u);
+          const bool next_ready = mbar_test(&tail->sf_full[next], next_phase);
+          const uint64_t da = da0 + static_cast<uint64_t>(stage * (F4_STAGE / 16));
+          const uint64_t db = db0 + static_cast<uint64_t>(stage * (F4_STAGE / 16));
+          const uint32_t sf = tmem + F4_SF_COL + stage * F4_SF_STAGE;
+          const int left = args.k - i * F4_BK;
+#pragma unroll
+          for (int j = 0; j < F4_BK / 64; ++j) {
+            if (j * 64 >= left) break;
+            // MXFP4: a 32-bit cell holds the scales of 128 values; the descriptor picks the half
+            const int group = kMx ? j >> 1 : j;
+            const uint32_t half = kMx ? static_cast<uint32_t>(j & 1) * 2 : 0u;
+            tc_mma_fp4_pair<FORMAT>(tmem, da + j * 2, db + j * 2, idesc | (half << 29) | (half << 4), sf + group * 4,
+                                    sf + F4_SF_N + group * 8, (i | j) != 0 ? 1u : 0u, leader);
+          }
+          tc_commit_pair(&tail->empty[stage], leader);
+          stage = next;
+          phase = next_phase;
+          ready = __all_sync(0xffffffffu, next_ready);
+        }
+        if (!ok) break;
+        tc_commit_pair(&tail->acc_full, leader);
+        acc_phase ^= 1;
+      }
+      if (!ok) {  // nothing may read shared memory or write TMEM after the CTAs are gone
+        tc_commit_pair(&tail->drain, leader);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&tail->drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp >= F4_FIRST_SF && warp < F4_FIRST_EPI) {
+    // ------------------------------------------------------------ scales -> TMEM
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int id = first_tile; id < total && ok; id += tile_stride) {
+      const Fp4Tile t = fp4_tile(args, id);
+      for (int i = 0; i < steps; ++i) {
+        ok = __all_sync(0xffffffffu, pair_wait(&tail->full[stage], phase, abort_flag));
+        if (!ok) break;
+        const uint8_t* sm = smem + stage * F4_STAGE + F4_OFF_SFM + lane * 16;
+        const uint8_t* sn = smem + stage * F4_STAGE + F4_OFF_SFN + lane * 16;
+        const uint32_t col = t_lane + F4_SF_COL + stage * F4_SF_STAGE;
+        // lane l takes rows l, l + 32, ...: row l + 32 q goes to column q (and 4 more for N rows
+        // from 128 on) of its K group
+        if constexpr (kMx) {
+          const int at = (i & 1) * 8;
+          uint32_t r[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sm + q * 512 + at);
+            r[q] = v.x;
+            r[4 + q] = v.y;
+          }
+          tmem_st_32x32b_x8(col, r);
+          uint32_t w[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sn + q * 512 + at);
+            w[q] = v.x;
+            w[8 + q] = v.y;
+          }
+          tmem_st_32x32b_x16(col + F4_SF_N, w);
+        } else {
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sm + q * 512);
+            r[q] = v.x;
+            r[4 + q] = v.y;
+            r[8 + q] = v.z;
+            r[12 + q] = v.w;
+          }
+          tmem_st_32x32b_x16(col, r);
+          uint32_t w[32];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sn + q * 512);
+            w[q] = v.x;
+            w[8 + q] = v.y;
+            w[16 + q] = v.z;
+            w[24 + q] = v.w;
+          }
+          tmem_st_32x32b_x32(col + F4_SF_N, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->sf_full[stage], 0));
+        if (++stage == F4_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp >= F4_FIRST_EPI) {
+    // ------------------------------------------------------------ results
+    const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;  // 64 columns of a lane quarter
+    const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
+    const bool pairs = OUT != kTypeFp32 && ((args.n | args.ldo) & 1) == 0;
+    uint32_t acc_phase = 0;
+    for (int id = first_tile; id < total; id += tile_stride) {
+      const Fp4Tile t = fp4_tile(args, id);
+      if (!__all_sync(0xffffffffu, pair_wait(&tail->acc_full, acc_phase, abort_flag))) break;
+      acc_phase ^= 1;
+      tc_fence_after();
+      const int c0 = part * 64;
+      uint32_t v[2][32];
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+      if (c0 < t.n) tmem_ld_32x32b_x32(from, v[0]);
+      if (c0 + 32 < t.n) tmem_ld_32x32b_x32(from + 32, v[1]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty, 0));
+      // a lane holds feature f of 32 consecutive rows, twice
+      const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = t.r0 + c0 + h * 32;
+        if (c0 + h * 32 >= t.n) break;
+        if constexpr (OUT == kTypeFp32) {
+          float* p = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo + f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (row + j < t.r_end && f < args.n) p[j * args.ldo] = __uint_as_float(v[h][j]) * scale;
+        } else if (pairs) {
+          // neighbouring lanes trade values, so that each stores two features of one row
+          const int odd = lane & 1;
+          uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row + odd) * args.ldo + (f - odd);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float mine = __uint_as_float(odd ? v[h][j + 1] : v[h][j]) * scale;
+            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[h][j] : v[h][j + 1], 1)) * scale;
+            const uint32_t w = odd ? pack_pair<OUT>(other, mine) : pack_pair<OUT>(mine, other);
+            if (row + j + odd < t.r_end && f < args.n) *reinterpret_cast<uint32_t*>(p + j * args.ldo) = w;
+          }
+        } else {  // rows that start on odd elements: one value at a time
+          uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row) * args.ldo + f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t w = pack_pair<OUT>(__uint_as_float(v[h][j]) * scale, 0.0f);
+            if (row + j < t.r_end && f < args.n) p[j * args.ldo] = static_cast<uint16_t>(w);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still signal or read it
+  tc_fence_after();
+  if (threadIdx.x == 0 && tail->abort_flag) atomicOr(&g_fp4_err, kErrTimeoutMma);
+  if (warp == 3) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host
+bool make_bytes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_cols,
+                    uint32_t box_rows, bool swizzle) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+  if (!enc) return false;
+  cuuint64_t dim[2] = {cols, rows};
+  cuuint64_t stride[1] = {pitch};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dim, stride, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FORMAT, int OUT>
+cudaError_t launch_fp4(const Fp4Args& a, const Fp4Maps& maps, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(gemm_fp4_kernel<FORMAT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kFp4Smem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((a.m + F4_TILE - 1) / F4_TILE) * ((a.n + F4_TILE - 1) / F4_TILE);
+  const int64_t pairs = std::min<int64_t>(sms / 2, tiles);
+  return launch_pdl(gemm_fp4_kernel<FORMAT, OUT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(F4_THREADS), kFp4Smem,
+                    s, a, maps);
+}
+
+template <int FORMAT>
+cudaError_t launch_format(int out_type, const Fp4Args& a, const Fp4Maps& maps, cudaStream_t s) {
+  if (out_type == kTypeBf16) return launch_fp4<FORMAT, kTypeBf16>(a, maps, s);
+  if (out_type == kTypeFp16) return launch_fp4<FORMAT, kTypeFp16>(a, maps, s);
+  return launch_fp4<FORMAT, kTypeFp32>(a, maps, s);
+}
+
+bool on(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+cudaError_t take_gemm_fp4_errors(uint32_t* bits, cudaStream_t s) { return take_error_word(g_fp4_err, bits, s); }
+
+}  // namespace beam
+
+using namespace beam;
+
+extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_codes, int64_t lda, const uint8_t* a_sf,
+                                             int64_t lda_sf, const float* alpha_a, const uint8_t* b_codes, int64_t ldb,
+                                             const uint8_t* b_sf, int64_t ldb_sf, const float* alpha_b, int32_t m,
+                                             int32_t n, int32_t k, void* out, int32_t out_type, int64_t ldo,
+                                             void* stream) {
+  if (m < 0 || n < 0 || k < 1 || (format != BEAM_MOE_FP4_MX && format != BEAM_MOE_FP4_NV)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (out_type != BEAM_MOE_BF16 && out_type != BEAM_MOE_FP16 && out_type != BEAM_MOE_FP32) return BEAM_MOE_ERR_INVALID_ARG;
+  if (k % 32 != 0 || m > 0x7fff0000 || n > 0x7fff0000) return BEAM_MOE_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(m) + 255) / 256 * ((static_cast<int64_t>(n) + 255) / 256) > INT32_MAX / 2)
+    return BEAM_MOE_ERR_UNSUPPORTED;
+  if (m == 0 || n == 0) return BEAM_MOE_OK;
+  const int64_t scales = k / (format == BEAM_MOE_FP4_MX ? 32 : 16);
+  if (!on(a_codes, 16) || !on(b_codes, 16) || !on(a_sf, 16) || !on(b_sf, 16) ||
+      !on(out, out_type == BEAM_MOE_FP32 ? 4 : 2))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if ((alpha_a && !on(alpha_a, 4)) || (alpha_b && !on(alpha_b, 4))) return BEAM_MOE_ERR_INVALID_ARG;
+  if (lda < k / 2 || ldb < k / 2 || lda % 16 != 0 || ldb % 16 != 0 || lda_sf < scales || ldb_sf < scales ||
+      lda_sf % 16 != 0 || ldb_sf % 16 != 0 || ldo < n)
+    return BEAM_MOE_ERR_INVALID_ARG;
+  const bool mx = format == BEAM_MOE_FP4_MX;
+  Fp4Maps maps;
+  if (!make_bytes_map(&maps.m_codes, b_codes, k / 2, n, ldb, 128, 128, true) ||
+      !make_bytes_map(&maps.n_codes, a_codes, k / 2, m, lda, 128, 128, true) ||
+      !make_bytes_map(&maps.n_codes32, a_codes, k / 2, m, lda, 128, F4_BOX, true) ||
+      !make_bytes_map(&maps.m_sf, b_sf, scales, n, ldb_sf, 16, 128, false) ||
+      !make_bytes_map(&maps.n_sf, a_sf, scales, m, lda_sf, 16, 256, false) ||
+      !make_bytes_map(&maps.n_sf32, a_sf, scales, m, lda_sf, 16, F4_BOX, false))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  // MXFP4 has no tensor scale
+  const Fp4Args args{m, n, k, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = mx ? launch_format<BEAM_MOE_FP4_MX>(out_type, args, maps, s)
+                           : launch_format<BEAM_MOE_FP4_NV>(out_type, args, maps, s);
+  return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA;
+}

@@ -465,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed_at(map_to_cta(&tail->acc_empty[acc], 0));
+        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty[acc], 0));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;

@@ -253,6 +253,7 @@ constexpr int kTypeBf16 = BEAM_MOE_BF16, kTypeFp16 = BEAM_MOE_FP16, kTypeFp32 = 
 void* tensor_map_encode_fn();
 // Error bits that this device's operators have set since the last call; synchronises s.
 cudaError_t take_grouped_gemm_errors(uint32_t* bits, cudaStream_t s);
+cudaError_t take_gemm_fp4_errors(uint32_t* bits, cudaStream_t s);
 template <class Symbol>
 cudaError_t take_error_word(Symbol& word, uint32_t* bits, cudaStream_t s) {
   cudaError_t e = cudaMemcpyFromSymbolAsync(bits, word, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);

@@ -1,0 +1,369 @@
+// 4-bit microscaled floating point: quantiser and its inverse, for 16-bit and FP32 tensors.
+//
+//   MXFP4  E2M1 codes, one UE8M0 byte per 32 values of a row: X = 2^e with e the smallest
+//          integer >= -127 such that amax <= 6 * 2^e (nothing saturates), q = E2M1(v / X),
+//          v / X exact;
+//   NVFP4  E2M1 codes, one E4M3 byte S per 16 values, one FP32 tensor scale alpha:
+//          S = E4M3(amax / (6 alpha)), q = E2M1(v / (S alpha)), every step an IEEE FP32
+//          operation (the rule of beam_moe_quantize_nvfp4, whose codes these are).
+// All roundings to nearest, ties to even.  A block that holds a NaN or an infinity gets a NaN
+// scale (0xFF, 0x7F) and zero codes, so that it reads back, and multiplies, as NaN.
+//
+// Bound by memory: a 16-bit value costs 2 bytes to read and 0.53 or 0.56 to write.  A lane
+// takes 8 consecutive values (one 16-byte load), so that a warp's load is 512 contiguous bytes,
+// its code store 128 and its scale store 8 or 16; a block's maximum is a shuffle over 4 or 2
+// lanes.  Each warp has four such pieces in flight.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "../../include/beam_moe.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace beam {
+
+namespace {
+
+constexpr int kMxFp4 = BEAM_MOE_FP4_MX;
+constexpr int kPieces = 4;      // pieces of 256 values that a warp has in flight
+constexpr int kPieceValues = 256;
+
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
+  if constexpr (TYPE == kTypeFp32) {
+    const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 q = __ldg(static_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kTypeBf16) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+// The largest |v| of 8 values as FP32 bits (which order like the values; NaN above infinity).
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// A row is cut into pieces of 256 values, the last one shorter; piece p of all the pieces.
+struct Piece {
+  int64_t row;
+  int col;     // the lane's first value
+  bool in;     // the lane's 8 values lie in the row
+};
+__device__ __forceinline__ Piece piece_of(int64_t p, int64_t total, int per_row, int cols, int lane) {
+  Piece r;
+  r.row = p / per_row;
+  r.col = static_cast<int>(p - r.row * per_row) * kPieceValues + lane * 8;
+  r.in = p < total && r.col < cols;
+  return r;
+}
+
+template <int TYPE, int FORMAT>
+__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, int64_t ld, int64_t rows,
+                                                           int cols, float alpha_param,
+                                                           const float* __restrict__ amax_dev,
+                                                           uint8_t* __restrict__ codes, int64_t ldc,
+                                                           uint8_t* __restrict__ sf, int64_t ldsf,
+                                                           float* __restrict__ alpha_out) {
+  constexpr bool kMx = FORMAT == kMxFp4;
+  constexpr int kSize = TYPE == kTypeFp32 ? 4 : 2;
+  constexpr int kLanes = kMx ? 4 : 2;  // lanes of one block
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
+  const int64_t total = rows * per_row;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  float alpha = 0.0f, six_alpha = 0.0f;
+  if (!kMx) {
+    alpha = amax_dev ? __fdiv_rn(*amax_dev, 2688.0f) : alpha_param;
+    six_alpha = __fmul_rn(6.0f, alpha);
+    if (alpha_out && blockIdx.x == 0 && threadIdx.x == 0) *alpha_out = alpha;
+  }
+  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
+       p0 += warps * kPieces) {
+    float v[kPieces][8];
+    Piece at[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      at[u] = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      if (at[u].in)
+        load8<TYPE>(static_cast<const uint8_t*>(src) + (at[u].row * ld + at[u].col) * kSize, v[u]);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      uint32_t m = amax8(v[u]);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      uint32_t scale, word = 0;
+      const bool finite = m < 0x7F800000u;
+      if constexpr (kMx) {
+        // amax = f * 2^E, f in [1, 2): 6 = 1.5 * 2^2, so e = E - 2 where f <= 1.5, else E - 1
+        int e = static_cast<int>(m >> 23) - 127 - 2 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+        e = max(e, -127);
+        scale = finite ? static_cast<uint32_t>(e + 127) : 0xFFu;
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e in [-127, 126]
+        if (finite) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            word |= cvt_e2m1x2(__fmul_rn(v[u][2 * i], inv), __fmul_rn(v[u][2 * i + 1], inv)) << (8 * i);
+        }
+      } else {
+        scale = alpha > 0.0f ? cvt_e4m3(__fdiv_rn(__uint_as_float(m), six_alpha)) : 0u;
+        if (!finite) scale = 0x7Fu;
+        if (finite && scale != 0) {
+          const float d = __fmul_rn(e4m3_value(scale), alpha);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            word |= cvt_e2m1x2(__fdiv_rn(v[u][2 * i], d), __fdiv_rn(v[u][2 * i + 1], d)) << (8 * i);
+        }
+      }
+      // four blocks' scales into one word, in the first lane of the four
+      uint32_t four = scale | (__shfl_down_sync(0xffffffffu, scale, kLanes) << 8);
+      four |= __shfl_down_sync(0xffffffffu, four, 2 * kLanes) << 16;
+      if (at[u].in) {
+        *reinterpret_cast<uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)) = word;
+        uint8_t* s = sf + at[u].row * ldsf + at[u].col / (8 * kLanes);
+        const int here = at[u].col & ~(32 * kLanes - 1);  // first value of the four blocks
+        if (here + 32 * kLanes <= cols) {
+          if (lane % (4 * kLanes) == 0) *reinterpret_cast<uint32_t*>(s) = four;
+        } else if (lane % kLanes == 0) {
+          *s = static_cast<uint8_t>(scale);
+        }
+      }
+    }
+  }
+}
+
+// The largest finite |v|, as FP32 bits.
+template <int TYPE>
+__global__ void __launch_bounds__(256) amax_finite_kernel(const void* __restrict__ src, int64_t ld, int64_t rows,
+                                                          int cols, unsigned int* __restrict__ out) {
+  constexpr int kSize = TYPE == kTypeFp32 ? 4 : 2;
+  const int lane = threadIdx.x & 31;
+  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
+  const int64_t total = rows * per_row, warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  uint32_t m = 0;
+  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
+       p0 += warps * kPieces) {
+    float v[kPieces][8];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const Piece at = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      if (at.in)
+        load8<TYPE>(static_cast<const uint8_t*>(src) + (at.row * ld + at.col) * kSize, v[u]);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(v[u][i]) & 0x7FFFFFFFu;
+        if (b < 0x7F800000u) m = max(m, b);
+      }
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  __shared__ uint32_t wm[8];
+  if (lane == 0) wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) m = max(m, wm[i]);
+    if (m) atomicMax(out, m);
+  }
+}
+
+// Two E2M1 codes (a byte) -> two FP32 values, exact.
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <int FORMAT, int OUT>
+__global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
+                                                             const uint8_t* __restrict__ sf, int64_t ldsf,
+                                                             const float* __restrict__ alpha_dev, int64_t rows,
+                                                             int cols, void* __restrict__ out, int64_t ldo) {
+  constexpr bool kMx = FORMAT == kMxFp4;
+  constexpr int kSize = OUT == kTypeFp32 ? 4 : 2;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
+  const int64_t total = rows * per_row;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const float alpha = !kMx && alpha_dev ? *alpha_dev : 1.0f;
+  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
+       p0 += warps * kPieces) {
+    uint32_t word[kPieces], scale[kPieces];
+    Piece at[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      at[u] = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      word[u] = scale[u] = 0;
+      if (at[u].in) {
+        word[u] = __ldg(reinterpret_cast<const uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)));
+        scale[u] = __ldg(sf + at[u].row * ldsf + at[u].col / (kMx ? 32 : 16));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      if (!at[u].in) continue;
+      float s;
+      if constexpr (kMx) {  // 2^(scale - 127); 0 is the subnormal 2^-127
+        s = scale[u] == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(scale[u] << 23);
+        if (scale[u] == 0xFFu) s = __uint_as_float(0x7FC00000u);
+      } else {
+        s = (scale[u] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(scale[u] & 0x7Fu);
+      }
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 q = e2m1x2_values((word[u] >> (8 * i)) & 0xFFu);
+        // code times block scale is exact; the tensor scale is one FP32 rounding
+        v[2 * i] = kMx ? __fmul_rn(q.x, s) : __fmul_rn(__fmul_rn(q.x, s), alpha);
+        v[2 * i + 1] = kMx ? __fmul_rn(q.y, s) : __fmul_rn(__fmul_rn(q.y, s), alpha);
+      }
+      uint8_t* p = static_cast<uint8_t*>(out) + (at[u].row * ldo + at[u].col) * kSize;
+      if constexpr (OUT == kTypeFp32) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (OUT == kTypeBf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+  }
+}
+
+// Warps of 256-value pieces, eight to a block, at most four pieces each before a grid of eight
+// blocks an SM repeats; few pieces get a block of their own each.
+unsigned grid_of(int64_t rows, int cols) {
+  const int64_t pieces = rows * ((cols + kPieceValues - 1) / kPieceValues);
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((pieces + 7) / 8, 148 * 8)));
+}
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+beam_moe_status launch_status(cudaError_t e) { return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA; }
+
+template <int TYPE>
+cudaError_t launch_quantize(int format, const void* src, int64_t ld, int64_t rows, int cols, float alpha,
+                            const float* amax_dev, uint8_t* codes, int64_t ldc, uint8_t* sf, int64_t ldsf,
+                            float* alpha_out, cudaStream_t s) {
+  auto k = format == kMxFp4 ? quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_MX> : quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_NV>;
+  return launch_pdl(k, dim3(grid_of(rows, cols)), dim3(256), 0, s, src, ld, rows, cols, alpha, amax_dev, codes, ldc,
+                    sf, ldsf, alpha_out);
+}
+
+template <int FORMAT>
+cudaError_t launch_dequantize(int out_type, const uint8_t* codes, int64_t ldc, const uint8_t* sf, int64_t ldsf,
+                              const float* alpha, int64_t rows, int cols, void* out, int64_t ldo, cudaStream_t s) {
+  auto k = out_type == kTypeBf16   ? dequantize_fp4_kernel<FORMAT, kTypeBf16>
+           : out_type == kTypeFp16 ? dequantize_fp4_kernel<FORMAT, kTypeFp16>
+                                   : dequantize_fp4_kernel<FORMAT, kTypeFp32>;
+  return launch_pdl(k, dim3(grid_of(rows, cols)), dim3(256), 0, s, codes, ldc, sf, ldsf, alpha, rows, cols, out, ldo);
+}
+
+beam_moe_status check_fp4(int32_t format, int64_t rows, int32_t cols, int32_t type) {
+  if (rows < 0 || cols < 0 || (format != BEAM_MOE_FP4_MX && format != BEAM_MOE_FP4_NV)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (type != BEAM_MOE_BF16 && type != BEAM_MOE_FP16 && type != BEAM_MOE_FP32) return BEAM_MOE_ERR_INVALID_ARG;
+  if (cols % 32 != 0 || rows > (int64_t{1} << 40)) return BEAM_MOE_ERR_UNSUPPORTED;
+  return BEAM_MOE_OK;
+}
+int scale_bytes(int32_t format, int32_t cols) { return cols / (format == BEAM_MOE_FP4_MX ? 32 : 16); }
+
+}  // namespace
+
+}  // namespace beam
+
+using namespace beam;
+
+extern "C" {
+
+beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t src_type, int64_t ld, int64_t rows,
+                                      int32_t cols, float alpha, uint8_t* codes, int64_t ldc, uint8_t* sf,
+                                      int64_t ldsf, float* alpha_out, void* stream) {
+  const beam_moe_status st = check_fp4(format, rows, cols, src_type);
+  if (st != BEAM_MOE_OK) return st;
+  if (rows == 0 || cols == 0) return BEAM_MOE_OK;
+  const int size = src_type == BEAM_MOE_FP32 ? 4 : 2;
+  if (!src || !codes || !sf || !aligned_to(src, 16) || !aligned_to(codes, 16) || !aligned_to(sf, 16))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (ld < cols || ld * size % 16 != 0 || ldc < cols / 2 || ldc % 16 != 0 || ldsf < scale_bytes(format, cols) ||
+      ldsf % 16 != 0)
+    return BEAM_MOE_ERR_INVALID_ARG;
+  const bool nv = format == BEAM_MOE_FP4_NV;
+  const bool given = alpha > 0.0f && alpha <= 3.4028235e38f;
+  if (nv && !given && (alpha > 0.0f || !alpha_out)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (nv && alpha_out && !aligned_to(alpha_out, 4)) return BEAM_MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const float* amax = nullptr;
+  if (nv && !given) {
+    // alpha_out first holds the largest value, then the scale
+    cudaError_t e = cudaMemsetAsync(alpha_out, 0, sizeof(float), s);
+    if (e != cudaSuccess) return BEAM_MOE_ERR_CUDA;
+    auto k = src_type == kTypeBf16   ? amax_finite_kernel<kTypeBf16>
+             : src_type == kTypeFp16 ? amax_finite_kernel<kTypeFp16>
+                                     : amax_finite_kernel<kTypeFp32>;
+    k<<<grid_of(rows, cols), 256, 0, s>>>(src, ld, rows, cols, reinterpret_cast<unsigned int*>(alpha_out));
+    if (cudaGetLastError() != cudaSuccess) return BEAM_MOE_ERR_CUDA;
+    amax = alpha_out;
+  }
+  auto run = src_type == kTypeBf16   ? launch_quantize<kTypeBf16>
+             : src_type == kTypeFp16 ? launch_quantize<kTypeFp16>
+                                     : launch_quantize<kTypeFp32>;
+  // a given scale is written by the quantiser; one that it reads as the amax, only after it
+  if (run(format, src, ld, rows, cols, alpha, amax, codes, ldc, sf, ldsf, amax ? nullptr : alpha_out, s) != cudaSuccess)
+    return BEAM_MOE_ERR_CUDA;
+  if (amax) return launch_status(launch_amax_to_alpha(alpha_out, s));
+  return BEAM_MOE_OK;
+}
+
+beam_moe_status beam_moe_dequantize_fp4(int32_t format, const uint8_t* codes, int64_t ldc, const uint8_t* sf,
+                                        int64_t ldsf, const float* alpha, int64_t rows, int32_t cols, void* out,
+                                        int32_t out_type, int64_t ldo, void* stream) {
+  const beam_moe_status st = check_fp4(format, rows, cols, out_type);
+  if (st != BEAM_MOE_OK) return st;
+  if (rows == 0 || cols == 0) return BEAM_MOE_OK;
+  const int size = out_type == BEAM_MOE_FP32 ? 4 : 2;
+  if (!codes || !sf || !out || !aligned_to(codes, 16) || !aligned_to(out, 16) || (alpha && !aligned_to(alpha, 4)))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (ldo < cols || ldo * size % 16 != 0 || ldc < cols / 2 || ldc % 16 != 0 || ldsf < scale_bytes(format, cols))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto run = format == BEAM_MOE_FP4_MX ? launch_dequantize<BEAM_MOE_FP4_MX> : launch_dequantize<BEAM_MOE_FP4_NV>;
+  return launch_status(run(out_type, codes, ldc, sf, ldsf, alpha, rows, cols, out, ldo, s));
+}
+
+}  // extern "C"

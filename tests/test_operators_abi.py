@@ -55,6 +55,80 @@ def test_grouped_products(name):
         assert _grouped(name, rows=2**31 - 2**17, n=2**30, k=2**30) == UNSUPPORTED
 
 
+def _quantize(form=0, src=P, t=bm.TYPE_BF16, ld=64, rows=4, cols=64, alpha=1.0, codes=P, ldc=32, sf=P, ldsf=16,
+              alpha_out=None):
+    return bm.lib().beam_moe_quantize_fp4(form, src, t, ld, rows, cols, alpha, codes, ldc, sf, ldsf, alpha_out, None)
+
+
+def _dequantize(form=0, codes=P, ldc=32, sf=P, ldsf=16, alpha=None, rows=4, cols=64, out=P, t=bm.TYPE_BF16, ldo=64):
+    return bm.lib().beam_moe_dequantize_fp4(form, codes, ldc, sf, ldsf, alpha, rows, cols, out, t, ldo, None)
+
+
+def _gemm(form=0, a=P, lda=32, asf=P, ldasf=16, alpha_a=None, b=P, ldb=32, bsf=P, ldbsf=16, alpha_b=None, m=4, n=8,
+          k=64, out=P, t=bm.TYPE_BF16, ldo=8):
+    return bm.lib().beam_moe_gemm_fp4(form, a, lda, asf, ldasf, alpha_a, b, ldb, bsf, ldbsf, alpha_b, m, n, k, out, t,
+                                      ldo, None)
+
+
+def test_fp4_quantiser():
+    for form in (bm.FP4_MX, bm.FP4_NV):
+        for call in (_quantize, _dequantize):
+            assert call(form=form, rows=-1) == BAD
+            assert call(form=form, cols=-32) == BAD
+            assert call(form=2) == BAD
+            assert call(form=form, t=3) == BAD
+            assert call(form=form, cols=48) == UNSUPPORTED
+            assert call(form=form, rows=0) == OK
+            assert call(form=form, cols=0) == OK
+            assert call(form=form, codes=None) == BAD
+            assert call(form=form, codes=P + 8) == BAD
+            assert call(form=form, sf=None) == BAD
+            assert call(form=form, ldc=16) == BAD
+            assert call(form=form, ldc=40) == BAD
+            assert call(form=form, ldsf=1) == BAD
+        assert _quantize(form=form, src=None) == BAD
+        assert _quantize(form=form, src=P + 2) == BAD
+        assert _quantize(form=form, ld=32) == BAD
+        assert _quantize(form=form, ld=68) == BAD
+        assert _quantize(form=form, sf=P + 4) == BAD
+        assert _quantize(form=form, ldsf=24) == BAD
+        assert _dequantize(form=form, out=None) == BAD
+        assert _dequantize(form=form, out=P + 2) == BAD
+        assert _dequantize(form=form, ldo=68) == BAD
+        assert _dequantize(form=form, alpha=P + 2) == BAD
+    assert _quantize(form=bm.FP4_NV, alpha=0.0) == BAD             # nowhere to put the scale found
+    assert _quantize(form=bm.FP4_NV, alpha=float("inf")) == BAD
+    assert _quantize(form=bm.FP4_NV, alpha_out=P + 2) == BAD
+
+
+def test_fp4_product():
+    for form in (bm.FP4_MX, bm.FP4_NV):
+        assert _gemm(form=form, m=-1) == BAD
+        assert _gemm(form=form, n=-1) == BAD
+        assert _gemm(form=form, k=0) == BAD
+        assert _gemm(form=form, k=48) == UNSUPPORTED
+        assert _gemm(form=form, m=2**31 - 1) == UNSUPPORTED
+        assert _gemm(form=form, m=2**30, n=2**30, ldo=2**30) == UNSUPPORTED
+        assert _gemm(form=form, t=5) == BAD
+        assert _gemm(form=form, m=0) == OK
+        assert _gemm(form=form, n=0) == OK
+        for name in ("a", "asf", "b", "bsf", "out"):
+            assert _gemm(form=form, **{name: None}) == BAD
+        for name in ("a", "asf", "b", "bsf"):
+            assert _gemm(form=form, **{name: P + 8}) == BAD
+        for name in ("lda", "ldb"):
+            assert _gemm(form=form, **{name: 16}) == BAD
+            assert _gemm(form=form, **{name: 40}) == BAD
+        for name in ("ldasf", "ldbsf"):
+            assert _gemm(form=form, **{name: 1}) == BAD
+            assert _gemm(form=form, **{name: 24}) == BAD
+        assert _gemm(form=form, ldo=7) == BAD
+        assert _gemm(form=form, out=P + 1) == BAD
+        assert _gemm(form=form, alpha_a=P + 1) == BAD
+        assert _gemm(form=form, alpha_b=P + 2) == BAD
+    assert _gemm(form=2) == BAD
+
+
 def test_tensors_have_to_be_on_a_gpu():
     x, w = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(2, 16, 32, dtype=torch.bfloat16)
     off = torch.zeros(3, dtype=torch.int32)
