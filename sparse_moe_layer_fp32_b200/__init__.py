@@ -344,32 +344,52 @@ def beam_moe_profile_read(h):
 
 
 # ------------------------------------------------------------------ operators on tensors
-def _on_one_device(*tensors):
-    """The CUDA device of all the tensors given (None stands for one that was not)."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError(f"the tensors have to be on one CUDA device, got {sorted(map(str, devices))}")
-    return next(iter(devices))
+# The smallest of these calls take a few microseconds on the GPU, so the checks below avoid
+# building objects: plain integers go to ctypes, and a stream is looked up by its number.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(name, device, *args, stream=None):
-    """Calls an entry point with `device` current, on `stream` or on that device's current one."""
-    with torch.cuda.device(device):
-        _check(getattr(_lib, name)(*args, _stream(stream)), name)
+def _device_index(first, *others):
+    """Number of the CUDA device that holds all the tensors (None stands for one not given)."""
+    device = first.device
+    same = device.type == "cuda"
+    for t in others:
+        if t is not None and t.device != device:
+            same = False
+    if not same:
+        raise ValueError("the tensors have to be on one CUDA device")
+    return device.index
+
+
+def _call(name, index, stream, *args):
+    """Calls an entry point with device `index` current, on `stream` or on that device's current one."""
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(_lib, name)(*args, raw)
+    if status != OK:
+        raise BeamMoeError(status, name)
 
 
 def _row_stride(t, what):
     """Elements from one row of a 2-D tensor to the next."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} has to be 2-D with its columns next to one another")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    if t.dim() != 2:
+        raise ValueError(f"{what} has to be 2-D")
+    rows, cols = t.shape
+    step, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}'s columns have to lie next to one another")
+    return step if rows > 1 else max(cols, step)
 
 
-def _grouped(offsets, *typed):
-    kind = typed[0].dtype
-    if kind not in (torch.bfloat16, torch.float16) or any(t.dtype != kind for t in typed):
+def _grouped(offsets, a, b):
+    kind = a.dtype
+    if (kind is not torch.bfloat16 and kind is not torch.float16) or b.dtype is not kind:
         raise ValueError("the operands have to be both BF16 or both FP16")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+    if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
         raise ValueError("offsets has to be a contiguous int32 vector of groups + 1 row numbers")
     return kind
 
@@ -377,8 +397,8 @@ def _grouped(offsets, *typed):
 def _output(out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype not in TYPES:
-        raise ValueError(f"out has to be a BF16, FP16 or FP32 tensor of shape {tuple(shape)}")
+    if out.shape != shape or out.dtype not in TYPES:
+        raise ValueError(f"out has to be a BF16, FP16 or FP32 tensor of shape {shape}")
     return out
 
 
@@ -392,15 +412,17 @@ def beam_moe_grouped_gemm(x, w, offsets, out=None, out_dtype=None, stream=None):
     """y[r] = w[e] x[r] for the rows r of each expert e, offsets[e] <= r < offsets[e + 1].
 
     x [rows, k] and w [groups, n, k] BF16 or FP16, offsets int32 [groups + 1], all on one device;
-    y [rows, n] in x's type or FP32 (out_dtype, or out's).  Rows of no expert are not written."""
+    y [rows, n] in x's type or FP32 (out's, else out_dtype, else x's).  Rows of no expert are not
+    written."""
     kind = _grouped(offsets, x, w)
     groups, n, k = _expert_weights(w, offsets)
     ldx = _row_stride(x, "x")
+    rows = x.shape[0]
     if x.shape[1] != k:
         raise ValueError(f"x has {x.shape[1]} columns and w {k}")
-    y = _output(out, (x.shape[0], n), out_dtype or kind, x.device)
-    _call("beam_moe_grouped_gemm", _on_one_device(x, w, offsets, y), _ptr(x), ldx, _ptr(w), _ptr(offsets), x.shape[0],
-          groups, n, k, TYPES[kind], _ptr(y), _row_stride(y, "out"), TYPES[y.dtype], stream=stream)
+    y = _output(out, (rows, n), out_dtype or kind, x.device)
+    _call("beam_moe_grouped_gemm", _device_index(x, w, offsets, y), stream, x.data_ptr(), ldx, w.data_ptr(),
+          offsets.data_ptr(), rows, groups, n, k, TYPES[kind], y.data_ptr(), _row_stride(y, "out"), TYPES[y.dtype])
     return y
 
 
@@ -412,11 +434,12 @@ def beam_moe_grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream
     kind = _grouped(offsets, dy, w)
     groups, n, k = _expert_weights(w, offsets)
     lddy = _row_stride(dy, "dy")
+    rows = dy.shape[0]
     if dy.shape[1] != n:
         raise ValueError(f"dy has {dy.shape[1]} columns and w {n} rows")
-    dx = _output(out, (dy.shape[0], k), out_dtype or kind, dy.device)
-    _call("beam_moe_grouped_gemm_dgrad", _on_one_device(dy, w, offsets, dx), _ptr(dy), lddy, _ptr(w), _ptr(offsets),
-          dy.shape[0], groups, n, k, TYPES[kind], _ptr(dx), _row_stride(dx, "out"), TYPES[dx.dtype], stream=stream)
+    dx = _output(out, (rows, k), out_dtype or kind, dy.device)
+    _call("beam_moe_grouped_gemm_dgrad", _device_index(dy, w, offsets, dx), stream, dy.data_ptr(), lddy, w.data_ptr(),
+          offsets.data_ptr(), rows, groups, n, k, TYPES[kind], dx.data_ptr(), _row_stride(dx, "out"), TYPES[dx.dtype])
     return dx
 
 
@@ -427,40 +450,43 @@ def beam_moe_grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, stream
     expert's is written; zero for one without rows)."""
     kind = _grouped(offsets, dy, x)
     lddy, ldx = _row_stride(dy, "dy"), _row_stride(x, "x")
-    if dy.shape[0] != x.shape[0]:
-        raise ValueError(f"dy has {dy.shape[0]} rows and x {x.shape[0]}")
-    groups, n, k = offsets.shape[0] - 1, dy.shape[1], x.shape[1]
+    rows, n = dy.shape
+    groups, k = offsets.shape[0] - 1, x.shape[1]
+    if x.shape[0] != rows:
+        raise ValueError(f"dy has {rows} rows and x {x.shape[0]}")
     dw = _output(out, (groups, n, k), out_dtype or kind, dy.device)
     if not dw.is_contiguous():
         raise ValueError("out has to be contiguous")
-    _call("beam_moe_grouped_gemm_wgrad", _on_one_device(dy, x, offsets, dw), _ptr(dy), lddy, _ptr(x), ldx,
-          _ptr(offsets), dy.shape[0], groups, n, k, TYPES[kind], _ptr(dw), TYPES[dw.dtype], stream=stream)
+    _call("beam_moe_grouped_gemm_wgrad", _device_index(dy, x, offsets, dw), stream, dy.data_ptr(), lddy, x.data_ptr(),
+          ldx, offsets.data_ptr(), rows, groups, n, k, TYPES[kind], dw.data_ptr(), TYPES[dw.dtype])
     return dw
 
 
 def _fp4_format(fmt):
-    if fmt not in FP4_FORMATS:
+    form = FP4_FORMATS.get(fmt)
+    if form is None:
         raise ValueError(f"unknown 4-bit format {fmt!r}")
-    return FP4_FORMATS[fmt]
+    return form
 
 
 def _fp4_matrix(codes, sf, fmt, what):
     """(rows, cols, bytes between rows of codes, of scales) of a quantised matrix."""
-    if codes.dtype != torch.uint8 or sf.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or sf.dtype is not torch.uint8:
         raise ValueError(f"{what}'s codes and scales have to be uint8 tensors")
-    rows, cols = codes.shape[0], codes.shape[1] * 2 if codes.dim() == 2 else 0
-    if codes.dim() != 2 or tuple(sf.shape) != (rows, cols // FP4_BLOCK[fmt]):
+    ldc, ldsf = _row_stride(codes, what), _row_stride(sf, what)
+    rows, half = codes.shape
+    blocks = 2 * half // FP4_BLOCK[fmt]
+    if sf.shape != (rows, blocks):
         raise ValueError(f"{what} has to be codes [rows, cols / 2] and scales [rows, cols / {FP4_BLOCK[fmt]}]")
-    ldc, ldsf = _row_stride(codes, f"{what}'s codes"), _row_stride(sf, f"{what}'s scales")
     if rows == 1:  # a single row's pitch is never stepped over: any that the library takes will do
-        ldsf = (max(ldsf, sf.shape[1]) + 15) // 16 * 16
-    return rows, cols, ldc, ldsf
+        ldsf = (ldsf + 15) // 16 * 16
+    return rows, 2 * half, ldc, ldsf
 
 
 def _tensor_scale(alpha, fmt, what):
     if alpha is None or fmt == "mxfp4":
         return None
-    if alpha.dtype != torch.float32 or alpha.numel() != 1:
+    if alpha.dtype is not torch.float32 or alpha.numel() != 1:
         raise ValueError(f"{what} has to be one FP32 value on the device")
     return alpha
 
@@ -473,25 +499,25 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     alpha is the tensor scale, a float; None takes the largest finite value / 2688, found on
     the device.  The alpha returned is an FP32 tensor [1] (None for MXFP4)."""
     form = _fp4_format(fmt)
-    if src.dtype not in TYPES:
+    kind = TYPES.get(src.dtype)
+    if kind is None:
         raise ValueError("src has to be BF16, FP16 or FP32")
+    if alpha is not None and not 0.0 < alpha < float("inf"):
+        raise ValueError("alpha has to be a positive finite number")
     ld = _row_stride(src, "src")
     rows, cols = src.shape
     blocks = cols // FP4_BLOCK[fmt]
-    device = _on_one_device(src)
+    pitch = (blocks + 15) // 16 * 16
+    index, device = _device_index(src), src.device
     codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-    sf = torch.empty((rows, (blocks + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    if alpha is not None and not 0.0 < float(alpha) < float("inf"):
-        raise ValueError("alpha has to be a positive finite number")
+    sf = torch.empty((rows, pitch), dtype=torch.uint8, device=device)
     scale = None
     if fmt == "nvfp4":  # the library writes it; an empty tensor has none
-        scale = (torch.empty if src.numel() else torch.zeros)(1, dtype=torch.float32, device=device)
-    with torch.cuda.device(device):
-        _check(_lib.beam_moe_quantize_fp4(form, _ptr(src), TYPES[src.dtype], ld, rows, cols,
-                                          ctypes.c_float(-1.0 if alpha is None else float(alpha)), _ptr(codes),
-                                          max(cols // 2, 16), _ptr(sf), max(sf.shape[1], 16), _ptr(scale),
-                                          _stream(stream)), "beam_moe_quantize_fp4")
-    return codes, sf[:, :blocks], scale
+        scale = (torch.empty if rows and cols else torch.zeros)(1, dtype=torch.float32, device=device)
+    _call("beam_moe_quantize_fp4", index, stream, form, src.data_ptr(), kind, ld, rows, cols,
+          -1.0 if alpha is None else alpha, codes.data_ptr(), cols // 2, sf.data_ptr(), pitch,
+          None if scale is None else scale.data_ptr())
+    return codes, sf if pitch == blocks else sf[:, :blocks], scale
 
 
 def beam_moe_dequantize_fp4(codes, sf, fmt, alpha=None, out_dtype=torch.bfloat16, stream=None):
@@ -501,10 +527,10 @@ def beam_moe_dequantize_fp4(codes, sf, fmt, alpha=None, out_dtype=torch.bfloat16
     alpha = _tensor_scale(alpha, fmt, "alpha")
     if out_dtype not in TYPES:
         raise ValueError("out_dtype has to be BF16, FP16 or FP32")
-    device = _on_one_device(codes, sf, alpha)
-    out = torch.empty((rows, cols), dtype=out_dtype, device=device)
-    _call("beam_moe_dequantize_fp4", device, form, _ptr(codes), ldc, _ptr(sf), ldsf, _ptr(alpha), rows, cols,
-          _ptr(out), TYPES[out_dtype], max(cols, 8), stream=stream)
+    index = _device_index(codes, sf, alpha)
+    out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
+    _call("beam_moe_dequantize_fp4", index, stream, form, codes.data_ptr(), ldc, sf.data_ptr(), ldsf,
+          None if alpha is None else alpha.data_ptr(), rows, cols, out.data_ptr(), TYPES[out_dtype], cols)
     return out
 
 
@@ -520,9 +546,10 @@ def beam_moe_gemm_fp4(a_codes, a_sf, b_codes, b_sf, fmt, alpha_a=None, alpha_b=N
         raise ValueError(f"a has {k} columns and b {kb}")
     alpha_a, alpha_b = _tensor_scale(alpha_a, fmt, "alpha_a"), _tensor_scale(alpha_b, fmt, "alpha_b")
     out = _output(out, (m, n), out_dtype or torch.bfloat16, a_codes.device)
-    _call("beam_moe_gemm_fp4", _on_one_device(a_codes, a_sf, b_codes, b_sf, alpha_a, alpha_b, out), form,
-          _ptr(a_codes), lda, _ptr(a_sf), lda_sf, _ptr(alpha_a), _ptr(b_codes), ldb, _ptr(b_sf), ldb_sf,
-          _ptr(alpha_b), m, n, k, _ptr(out), TYPES[out.dtype], _row_stride(out, "out"), stream=stream)
+    _call("beam_moe_gemm_fp4", _device_index(a_codes, a_sf, b_codes, b_sf, alpha_a, alpha_b, out), stream, form,
+          a_codes.data_ptr(), lda, a_sf.data_ptr(), lda_sf, None if alpha_a is None else alpha_a.data_ptr(),
+          b_codes.data_ptr(), ldb, b_sf.data_ptr(), ldb_sf, None if alpha_b is None else alpha_b.data_ptr(), m, n, k,
+          out.data_ptr(), TYPES[out.dtype], _row_stride(out, "out"))
     return out
 
 

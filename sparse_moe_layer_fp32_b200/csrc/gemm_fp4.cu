@@ -46,7 +46,6 @@ constexpr int F4_OFF_SFN = F4_OFF_SFM + 128 * 16;
 constexpr int F4_STAGE = F4_OFF_SFN + 256 * 16;
 static_assert(F4_STAGE % 1024 == 0, "swizzled lines start on 1 KB boundaries");
 constexpr int F4_TILE = 256;
-constexpr int F4_BOX = 32;                      // rows of a short load
 constexpr int F4_PANEL = 8;                     // row blocks of A that share B in turn
 constexpr int F4_SF_COL = 256;                  // TMEM columns of the stages' scales
 constexpr int F4_SF_STAGE = 48;                 // M: 4 columns per K group, then N: 8 per K group
@@ -57,6 +56,7 @@ constexpr int F4_THREADS = 32 * (F4_FIRST_EPI + F4_EPI_WARPS);
 
 struct Fp4Args {
   int m, n, k;             // D is [m][n]
+  int blocks, height;      // A's rows in equal blocks, their height a multiple of 32 up to 256
   const float* alpha_a;    // tensor scales, or nullptr
   const float* alpha_b;
   void* out;
@@ -85,15 +85,13 @@ struct Fp4Tile {
 __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& a, int id) {
   Fp4Tile t;
   const int ft = (a.n + F4_TILE - 1) / F4_TILE;
-  const int blocks = (a.m + F4_TILE - 1) / F4_TILE;
   const int panel = id / (F4_PANEL * ft);
   const int rest = id - panel * F4_PANEL * ft;
-  const int wide = min(F4_PANEL, blocks - panel * F4_PANEL);
+  const int wide = min(F4_PANEL, a.blocks - panel * F4_PANEL);
   t.f0 = rest / wide * F4_TILE;
   const int block = panel * F4_PANEL + rest % wide;
-  const int height = ((a.m + blocks - 1) / blocks + 31) & ~31;  // equal blocks
-  t.r0 = block * height;
-  t.r_end = min(a.m, t.r0 + height);
+  t.r0 = block * a.height;
+  t.r_end = min(a.m, t.r0 + a.height);
   t.n = max(32, (t.r_end - t.r0 + 31) & ~31);
   return t;
 }
@@ -131,8 +129,10 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   }
 }
 
+// Boxes: 128 rows of B; half a block's and a whole block's rows of A (the last block is shorter:
+// what its boxes bring of later rows, or zeros, feeds accumulator columns that are not stored).
 struct Fp4Maps {
-  CUtensorMap m_codes, n_codes, n_codes32, m_sf, n_sf, n_sf32;
+  CUtensorMap m_codes, n_codes, m_sf, n_sf;
 };
 
 template <int FORMAT, int OUT>
@@ -172,7 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
   pdl_wait();
   pdl_trigger();
   const uint32_t tmem = tail->tmem_base;
-  const int total = ((args.m + F4_TILE - 1) / F4_TILE) * ((args.n + F4_TILE - 1) / F4_TILE);
+  const int total = args.blocks * ((args.n + F4_TILE - 1) / F4_TILE);
   const int first_tile = blockIdx.x >> 1, tile_stride = gridDim.x >> 1;
   const int steps = (args.k + F4_BK - 1) / F4_BK;
 
@@ -181,13 +181,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    const uint32_t bytes = F4_CODES + 128 * 16 + static_cast<uint32_t>(args.height) * (128 / 2 + 16);
     for (int id = first_tile; id < total && ok; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
       const int half = t.n >> 1;
       const int f0 = t.f0 + static_cast<int>(rank) * 128, r0 = t.r0 + static_cast<int>(rank) * half;
-      const int code_boxes = (half + F4_BOX - 1) / F4_BOX, sf_boxes = t.n / F4_BOX;
-      const uint32_t bytes = F4_CODES + 128 * 16 + static_cast<uint32_t>(code_boxes) * F4_BOX * 128 +
-                             static_cast<uint32_t>(sf_boxes) * F4_BOX * 16;
       for (int i = 0; i < steps; ++i) {
         ok = __all_sync(0xffffffffu, pair_wait(&tail->empty[stage], phase ^ 1, abort_flag));
         if (!ok) break;
@@ -199,15 +197,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
           mbar_arrive_expect_tx(bar, bytes);
           tma_load_2d(s, &maps.m_codes, bar, i * 128, f0);
           tma_load_2d(s + F4_OFF_SFM, &maps.m_sf, bar, sx, f0);
-          if (half == 128) {
-            tma_load_2d(s + F4_OFF_N, &maps.n_codes, bar, i * 128, r0);
-            tma_load_2d(s + F4_OFF_SFN, &maps.n_sf, bar, sx, t.r0);
-          } else {
-            for (int b = 0; b < code_boxes; ++b)
-              tma_load_2d(s + F4_OFF_N + b * F4_BOX * 128, &maps.n_codes32, bar, i * 128, r0 + b * F4_BOX);
-            for (int b = 0; b < sf_boxes; ++b)
-              tma_load_2d(s + F4_OFF_SFN + b * F4_BOX * 16, &maps.n_sf32, bar, sx, t.r0 + b * F4_BOX);
-          }
+          tma_load_2d(s + F4_OFF_N, &maps.n_codes, bar, i * 128, r0);
+          tma_load_2d(s + F4_OFF_SFN, &maps.n_sf, bar, sx, t.r0);
         }
         __syncwarp();
         if (++stage == F4_STAGES) {
@@ -425,7 +416,7 @@ cudaError_t launch_fp4(const Fp4Args& a, const Fp4Maps& maps, cudaStream_t s) {
     e = cudaFuncSetAttribute(gemm_fp4_kernel<FORMAT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kFp4Smem));
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((a.m + F4_TILE - 1) / F4_TILE) * ((a.n + F4_TILE - 1) / F4_TILE);
+  const int64_t tiles = static_cast<int64_t>(a.blocks) * ((a.n + F4_TILE - 1) / F4_TILE);
   const int64_t pairs = std::min<int64_t>(sms / 2, tiles);
   return launch_pdl(gemm_fp4_kernel<FORMAT, OUT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(F4_THREADS), kFp4Smem,
                     s, a, maps);
@@ -468,16 +459,16 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
       lda_sf % 16 != 0 || ldb_sf % 16 != 0 || ldo < n)
     return BEAM_MOE_ERR_INVALID_ARG;
   const bool mx = format == BEAM_MOE_FP4_MX;
+  const int blocks = (m + F4_TILE - 1) / F4_TILE;
+  const int height = ((m + blocks - 1) / blocks + 31) / 32 * 32;
   Fp4Maps maps;
   if (!make_bytes_map(&maps.m_codes, b_codes, k / 2, n, ldb, 128, 128, true) ||
-      !make_bytes_map(&maps.n_codes, a_codes, k / 2, m, lda, 128, 128, true) ||
-      !make_bytes_map(&maps.n_codes32, a_codes, k / 2, m, lda, 128, F4_BOX, true) ||
+      !make_bytes_map(&maps.n_codes, a_codes, k / 2, m, lda, 128, height / 2, true) ||
       !make_bytes_map(&maps.m_sf, b_sf, scales, n, ldb_sf, 16, 128, false) ||
-      !make_bytes_map(&maps.n_sf, a_sf, scales, m, lda_sf, 16, 256, false) ||
-      !make_bytes_map(&maps.n_sf32, a_sf, scales, m, lda_sf, 16, F4_BOX, false))
+      !make_bytes_map(&maps.n_sf, a_sf, scales, m, lda_sf, 16, height, false))
     return BEAM_MOE_ERR_INVALID_ARG;
   // MXFP4 has no tensor scale
-  const Fp4Args args{m, n, k, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
+  const Fp4Args args{m, n, k, blocks, height, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mx ? launch_format<BEAM_MOE_FP4_MX>(out_type, args, maps, s)
                            : launch_format<BEAM_MOE_FP4_NV>(out_type, args, maps, s);

@@ -60,23 +60,43 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   return m;
 }
 
-// A row is cut into pieces of 256 values, the last one shorter; piece p of all the pieces.
-struct Piece {
-  int64_t row;
-  int col;     // the lane's first value
-  bool in;     // the lane's 8 values lie in the row
+// A matrix cut into pieces of 256 values of a row, the last one of a row shorter.  A matrix whose
+// rows lie end to end in every array is one long row.  Rows are split from piece numbers by
+// a multiplication: magic = min(2^32 - 1, floor(2^32 / per_row)) is too small by less than one.
+struct Pieces {
+  uint32_t total, per_row, magic;
 };
-__device__ __forceinline__ Piece piece_of(int64_t p, int64_t total, int per_row, int cols, int lane) {
+struct Piece {
+  uint32_t row;
+  int64_t col;  // the lane's first value
+  bool in;      // the lane's 8 values lie in the row
+};
+__device__ __forceinline__ Piece piece_of(const Pieces& s, uint32_t p, int64_t cols, int lane) {
   Piece r;
-  r.row = p / per_row;
-  r.col = static_cast<int>(p - r.row * per_row) * kPieceValues + lane * 8;
-  r.in = p < total && r.col < cols;
+  r.row = __umulhi(p, s.magic);
+  uint32_t rest = p - r.row * s.per_row;
+  if (rest >= s.per_row) {
+    ++r.row;
+    rest -= s.per_row;
+  }
+  r.col = static_cast<int64_t>(rest) * kPieceValues + lane * 8;
+  r.in = p < s.total && r.col < cols;
   return r;
 }
 
+// E2M1 of v / d with the quotient of IEEE FP32 division, r the reciprocal of d.  q = v r is
+// within 2 units in the last place of the quotient, so both have the same code unless q lies
+// that close to a border between two codes (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5: the 21 low bits
+// of a border are zero) and is not the exact quotient; only then is the division done.
+__device__ __forceinline__ float quotient_for_e2m1(float v, float d, float r) {
+  float q = __fmul_rn(v, r);
+  if (((__float_as_uint(q) + 8u) & 0x1FFFFFu) < 16u && __fmaf_rn(-q, d, v) != 0.0f) q = __fdiv_rn(v, d);
+  return q;
+}
+
 template <int TYPE, int FORMAT>
-__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, int64_t ld, int64_t rows,
-                                                           int cols, float alpha_param,
+__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, int64_t ld, Pieces pieces,
+                                                           int64_t cols, float alpha_param,
                                                            const float* __restrict__ amax_dev,
                                                            uint8_t* __restrict__ codes, int64_t ldc,
                                                            uint8_t* __restrict__ sf, int64_t ldsf,
@@ -87,22 +107,19 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
-  const int64_t total = rows * per_row;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const uint32_t warps = gridDim.x * 8u;
   float alpha = 0.0f, six_alpha = 0.0f;
   if (!kMx) {
     alpha = amax_dev ? __fdiv_rn(*amax_dev, 2688.0f) : alpha_param;
     six_alpha = __fmul_rn(6.0f, alpha);
     if (alpha_out && blockIdx.x == 0 && threadIdx.x == 0) *alpha_out = alpha;
   }
-  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
-       p0 += warps * kPieces) {
+  for (uint32_t p0 = blockIdx.x * 8u + (threadIdx.x >> 5); p0 < pieces.total; p0 += warps * kPieces) {
     float v[kPieces][8];
     Piece at[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      at[u] = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      at[u] = piece_of(pieces, p0 + u * warps, cols, lane);
       if (at[u].in)
         load8<TYPE>(static_cast<const uint8_t*>(src) + (at[u].row * ld + at[u].col) * kSize, v[u]);
       else
@@ -132,9 +149,17 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
         if (!finite) scale = 0x7Fu;
         if (finite && scale != 0) {
           const float d = __fmul_rn(e4m3_value(scale), alpha);
+          const float r = __frcp_rn(d);
+          if (d >= 0x1p-100f && d <= 0x1p100f) {  // no step of the short form leaves FP32's normal range
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            word |= cvt_e2m1x2(__fdiv_rn(v[u][2 * i], d), __fdiv_rn(v[u][2 * i + 1], d)) << (8 * i);
+            for (int i = 0; i < 4; ++i)
+              word |= cvt_e2m1x2(quotient_for_e2m1(v[u][2 * i], d, r), quotient_for_e2m1(v[u][2 * i + 1], d, r))
+                      << (8 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              word |= cvt_e2m1x2(__fdiv_rn(v[u][2 * i], d), __fdiv_rn(v[u][2 * i + 1], d)) << (8 * i);
+          }
         }
       }
       // four blocks' scales into one word, in the first lane of the four
@@ -143,7 +168,7 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
       if (at[u].in) {
         *reinterpret_cast<uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)) = word;
         uint8_t* s = sf + at[u].row * ldsf + at[u].col / (8 * kLanes);
-        const int here = at[u].col & ~(32 * kLanes - 1);  // first value of the four blocks
+        const int64_t here = at[u].col & ~static_cast<int64_t>(32 * kLanes - 1);  // first value of the four blocks
         if (here + 32 * kLanes <= cols) {
           if (lane % (4 * kLanes) == 0) *reinterpret_cast<uint32_t*>(s) = four;
         } else if (lane % kLanes == 0) {
@@ -156,19 +181,17 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
 
 // The largest finite |v|, as FP32 bits.
 template <int TYPE>
-__global__ void __launch_bounds__(256) amax_finite_kernel(const void* __restrict__ src, int64_t ld, int64_t rows,
-                                                          int cols, unsigned int* __restrict__ out) {
+__global__ void __launch_bounds__(256) amax_finite_kernel(const void* __restrict__ src, int64_t ld, Pieces pieces,
+                                                          int64_t cols, unsigned int* __restrict__ out) {
   constexpr int kSize = TYPE == kTypeFp32 ? 4 : 2;
   const int lane = threadIdx.x & 31;
-  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
-  const int64_t total = rows * per_row, warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const uint32_t warps = gridDim.x * 8u;
   uint32_t m = 0;
-  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
-       p0 += warps * kPieces) {
+  for (uint32_t p0 = blockIdx.x * 8u + (threadIdx.x >> 5); p0 < pieces.total; p0 += warps * kPieces) {
     float v[kPieces][8];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const Piece at = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      const Piece at = piece_of(pieces, p0 + u * warps, cols, lane);
       if (at.in)
         load8<TYPE>(static_cast<const uint8_t*>(src) + (at.row * ld + at.col) * kSize, v[u]);
       else
@@ -203,24 +226,21 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 template <int FORMAT, int OUT>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                              const uint8_t* __restrict__ sf, int64_t ldsf,
-                                                             const float* __restrict__ alpha_dev, int64_t rows,
-                                                             int cols, void* __restrict__ out, int64_t ldo) {
+                                                             const float* __restrict__ alpha_dev, Pieces pieces,
+                                                             int64_t cols, void* __restrict__ out, int64_t ldo) {
   constexpr bool kMx = FORMAT == kMxFp4;
   constexpr int kSize = OUT == kTypeFp32 ? 4 : 2;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int per_row = (cols + kPieceValues - 1) / kPieceValues;
-  const int64_t total = rows * per_row;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const uint32_t warps = gridDim.x * 8u;
   const float alpha = !kMx && alpha_dev ? *alpha_dev : 1.0f;
-  for (int64_t p0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); p0 < total;
-       p0 += warps * kPieces) {
+  for (uint32_t p0 = blockIdx.x * 8u + (threadIdx.x >> 5); p0 < pieces.total; p0 += warps * kPieces) {
     uint32_t word[kPieces], scale[kPieces];
     Piece at[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      at[u] = piece_of(p0 + u * warps, total, per_row, cols, lane);
+      at[u] = piece_of(pieces, p0 + u * warps, cols, lane);
       word[u] = scale[u] = 0;
       if (at[u].in) {
         word[u] = __ldg(reinterpret_cast<const uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)));
@@ -267,11 +287,29 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
   }
 }
 
-// Warps of 256-value pieces, eight to a block, at most four pieces each before a grid of eight
-// blocks an SM repeats; few pieces get a block of their own each.
-unsigned grid_of(int64_t rows, int cols) {
-  const int64_t pieces = rows * ((cols + kPieceValues - 1) / kPieceValues);
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((pieces + 7) / 8, 148 * 8)));
+// Eight warps to a block; a grid of up to eight blocks an SM, each warp at most four pieces
+// before it repeats.
+unsigned grid_of(const Pieces& p) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((int64_t{p.total} + 7) / 8, 148 * 8)));
+}
+// One launch's share of a matrix: at most kMaxPieces pieces, so that their numbers (and the steps
+// of a loop past the last one) fit 32 bits.
+constexpr int64_t kMaxPieces = int64_t{1} << 30;
+Pieces pieces_of(int64_t rows, int64_t cols) {
+  const int64_t per_row = (cols + kPieceValues - 1) / kPieceValues;
+  return Pieces{static_cast<uint32_t>(rows * per_row), static_cast<uint32_t>(per_row),
+                static_cast<uint32_t>(std::min<int64_t>((int64_t{1} << 32) / per_row, 0xFFFFFFFFll))};
+}
+// Calls f(first row, rows, columns) for shares of the matrix, one long row where `flat`.
+template <class F>
+cudaError_t for_shares(int64_t rows, int64_t cols, bool flat, F f) {
+  if (flat && (rows * cols + kPieceValues - 1) / kPieceValues <= kMaxPieces) return f(int64_t{0}, int64_t{1}, rows * cols);
+  const int64_t most = std::max<int64_t>(1, kMaxPieces / ((cols + kPieceValues - 1) / kPieceValues));
+  for (int64_t r = 0; r < rows; r += most) {
+    const cudaError_t e = f(r, std::min(most, rows - r), cols);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -282,8 +320,26 @@ cudaError_t launch_quantize(int format, const void* src, int64_t ld, int64_t row
                             const float* amax_dev, uint8_t* codes, int64_t ldc, uint8_t* sf, int64_t ldsf,
                             float* alpha_out, cudaStream_t s) {
   auto k = format == kMxFp4 ? quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_MX> : quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_NV>;
-  return launch_pdl(k, dim3(grid_of(rows, cols)), dim3(256), 0, s, src, ld, rows, cols, alpha, amax_dev, codes, ldc,
-                    sf, ldsf, alpha_out);
+  const bool flat = ld == cols && ldc == cols / 2 && ldsf == cols / (format == kMxFp4 ? 32 : 16);
+  return for_shares(rows, cols, flat, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c);
+    return launch_pdl(k, dim3(grid_of(p)), dim3(256), 0, s,
+                      static_cast<const uint8_t*>(src) + r * ld * (TYPE == kTypeFp32 ? 4 : 2), ld, p, c, alpha,
+                      amax_dev, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha_out);
+  });
+}
+
+template <int TYPE>
+cudaError_t launch_amax_finite(const void* src, int64_t ld, int64_t rows, int cols, float* out, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(out, 0, sizeof(float), s);
+  if (e != cudaSuccess) return e;
+  return for_shares(rows, cols, ld == cols, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c);
+    amax_finite_kernel<TYPE><<<grid_of(p), 256, 0, s>>>(
+        static_cast<const uint8_t*>(src) + r * ld * (TYPE == kTypeFp32 ? 4 : 2), ld, p, c,
+        reinterpret_cast<unsigned int*>(out));
+    return cudaGetLastError();
+  });
 }
 
 template <int FORMAT>
@@ -292,7 +348,12 @@ cudaError_t launch_dequantize(int out_type, const uint8_t* codes, int64_t ldc, c
   auto k = out_type == kTypeBf16   ? dequantize_fp4_kernel<FORMAT, kTypeBf16>
            : out_type == kTypeFp16 ? dequantize_fp4_kernel<FORMAT, kTypeFp16>
                                    : dequantize_fp4_kernel<FORMAT, kTypeFp32>;
-  return launch_pdl(k, dim3(grid_of(rows, cols)), dim3(256), 0, s, codes, ldc, sf, ldsf, alpha, rows, cols, out, ldo);
+  const bool flat = ldo == cols && ldc == cols / 2 && ldsf == cols / (FORMAT == kMxFp4 ? 32 : 16);
+  return for_shares(rows, cols, flat, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c);
+    return launch_pdl(k, dim3(grid_of(p)), dim3(256), 0, s, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha, p, c,
+                      static_cast<void*>(static_cast<uint8_t*>(out) + r * ldo * (out_type == kTypeFp32 ? 4 : 2)), ldo);
+  });
 }
 
 beam_moe_status check_fp4(int32_t format, int64_t rows, int32_t cols, int32_t type) {
@@ -331,13 +392,10 @@ beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t s
   const float* amax = nullptr;
   if (nv && !given) {
     // alpha_out first holds the largest value, then the scale
-    cudaError_t e = cudaMemsetAsync(alpha_out, 0, sizeof(float), s);
-    if (e != cudaSuccess) return BEAM_MOE_ERR_CUDA;
-    auto k = src_type == kTypeBf16   ? amax_finite_kernel<kTypeBf16>
-             : src_type == kTypeFp16 ? amax_finite_kernel<kTypeFp16>
-                                     : amax_finite_kernel<kTypeFp32>;
-    k<<<grid_of(rows, cols), 256, 0, s>>>(src, ld, rows, cols, reinterpret_cast<unsigned int*>(alpha_out));
-    if (cudaGetLastError() != cudaSuccess) return BEAM_MOE_ERR_CUDA;
+    auto find = src_type == kTypeBf16   ? launch_amax_finite<kTypeBf16>
+                : src_type == kTypeFp16 ? launch_amax_finite<kTypeFp16>
+                                        : launch_amax_finite<kTypeFp32>;
+    if (find(src, ld, rows, cols, alpha_out, s) != cudaSuccess) return BEAM_MOE_ERR_CUDA;
     amax = alpha_out;
   }
   auto run = src_type == kTypeBf16   ? launch_quantize<kTypeBf16>
