@@ -9,10 +9,11 @@
 // All roundings to nearest, ties to even.  A block that holds a NaN or an infinity gets a NaN
 // scale (0xFF, 0x7F) and zero codes, so that it reads back, and multiplies, as NaN.
 //
-// Bound by memory: a 16-bit value costs 2 bytes to read and 0.53 or 0.56 to write.  A lane
-// takes 8 consecutive values (one 16-byte load), so that a warp's load is 512 contiguous bytes,
-// its code store 128 and its scale store 8 or 16; a block's maximum is a shuffle over 4 or 2
-// lanes.  Each warp has four such pieces in flight.
+// Bound by memory: a 16-bit value costs 2 bytes to read and 0.53 or 0.56 to write.  The quantiser
+// gives a thread a whole block (16 or 32 values), so that the block's scale is worked out once
+// and without a shuffle; four lanes to a block of 8 values each, with its wider loads, spent the
+// time on the scales instead (16384 x 5120 BF16: MXFP4 57, NVFP4 107 us).  The inverse gives a
+// lane 8 values, whose store is then 16 bytes.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -52,20 +53,73 @@ __device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
   }
 }
 
-// The largest |v| of 8 values as FP32 bits (which order like the values; NaN above infinity).
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+// One 32-byte load of memory that the kernel does not write, from a 32-byte boundary.
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
 }
 
-// A matrix cut into pieces of 256 values of a row, the last one of a row shorter.  A matrix whose
-// rows lie end to end in every array is one long row.  Rows are split from piece numbers by
+// A block as it lies in memory, in 32-bit words (two 16-bit values or one FP32 value each).
+template <int TYPE, int N>
+struct RawBlock {
+  static constexpr int kPer = TYPE == kTypeFp32 ? 1 : 2;
+  static constexpr int kWords = N / kPer;
+  uint32_t w[kWords];
+  // wide: p lies on a 32-byte boundary
+  __device__ __forceinline__ void load(const void* p, bool wide) {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8) ld_global_v8(static_cast<const uint32_t*>(p) + i, w + i);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 q = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (TYPE == kTypeFp32) return __uint_as_float(w[i]);
+    else if constexpr (TYPE == kTypeBf16) return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    else {
+      const __half2 h = *reinterpret_cast<const __half2*>(&w[i / 2]);
+      return (i & 1) ? __high2float(h) : __low2float(h);
+    }
+  }
+  // The largest |v| as FP32 bits, which order like the values (NaN above infinity).  Of 16-bit
+  // values, two maxima at a time on their own bits, which order likewise.
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+    if constexpr (TYPE == kTypeFp32) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      m = max(m >> 16, m & 0xFFFFu);
+      if constexpr (TYPE == kTypeBf16) return m << 16;
+      else return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    }
+  }
+};
+
+// A matrix cut into pieces, per_row to a row: blocks of 16 or 32 values, or 256 values of a row,
+// the last such piece of a row shorter.  A matrix whose rows lie end to end in every array is one
+// long row.  Rows are split from piece numbers by
 // a multiplication: magic = min(2^32 - 1, floor(2^32 / per_row)) is too small by less than one.
 struct Pieces {
   uint32_t total, per_row, magic;
 };
+__device__ __forceinline__ void split_piece(const Pieces& s, uint32_t p, uint32_t& row, uint32_t& rest) {
+  row = __umulhi(p, s.magic);
+  rest = p - row * s.per_row;
+  if (rest >= s.per_row) {
+    ++row;
+    rest -= s.per_row;
+  }
+}
 struct Piece {
   uint32_t row;
   int64_t col;  // the lane's first value
@@ -73,66 +127,62 @@ struct Piece {
 };
 __device__ __forceinline__ Piece piece_of(const Pieces& s, uint32_t p, int64_t cols, int lane) {
   Piece r;
-  r.row = __umulhi(p, s.magic);
-  uint32_t rest = p - r.row * s.per_row;
-  if (rest >= s.per_row) {
-    ++r.row;
-    rest -= s.per_row;
-  }
+  uint32_t rest;
+  split_piece(s, p, r.row, rest);
   r.col = static_cast<int64_t>(rest) * kPieceValues + lane * 8;
   r.in = p < s.total && r.col < cols;
   return r;
 }
 
-// E2M1 of v / d with the quotient of IEEE FP32 division, r the reciprocal of d.  q = v r is
-// within 2 units in the last place of the quotient, so both have the same code unless q lies
-// that close to a border between two codes (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5: the 21 low bits
-// of a border are zero) and is not the exact quotient; only then is the division done.
-__device__ __forceinline__ float quotient_for_e2m1(float v, float d, float r) {
+// v / d rounded to nearest, r = 1 / d rounded to nearest.  Markstein's division (IBM J. Res. Dev.
+// 34, 1990): with the reciprocal so rounded and q within a unit in the last place, q plus r times
+// the remainder v - q d rounds to the quotient.  v r is within two units, the first step brings
+// it within one, the second is exact; neither branches, and the remainder is one fused operation.
+// Holds while nothing leaves the normal range (a quotient that does is a zero code all the same).
+__device__ __forceinline__ float quotient(float v, float d, float r) {
   float q = __fmul_rn(v, r);
-  if (((__float_as_uint(q) + 8u) & 0x1FFFFFu) < 16u && __fmaf_rn(-q, d, v) != 0.0f) q = __fdiv_rn(v, d);
-  return q;
+  q = __fmaf_rn(__fmaf_rn(-q, d, v), r, q);
+  return __fmaf_rn(__fmaf_rn(-q, d, v), r, q);
 }
 
 template <int TYPE, int FORMAT>
-__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, int64_t ld, Pieces pieces,
-                                                           int64_t cols, float alpha_param,
-                                                           const float* __restrict__ amax_dev,
+__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, int64_t ld, Pieces blocks,
+                                                           float alpha_param, const float* __restrict__ amax_dev,
                                                            uint8_t* __restrict__ codes, int64_t ldc,
                                                            uint8_t* __restrict__ sf, int64_t ldsf,
-                                                           float* __restrict__ alpha_out) {
+                                                           float* __restrict__ alpha_out, bool wide) {
   constexpr bool kMx = FORMAT == kMxFp4;
   constexpr int kSize = TYPE == kTypeFp32 ? 4 : 2;
-  constexpr int kLanes = kMx ? 4 : 2;  // lanes of one block
+  constexpr int N = kMx ? 32 : 16;
+  constexpr int kAtOnce = N * kSize <= 64 ? 2 : 1;  // blocks a thread has in flight
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const uint32_t warps = gridDim.x * 8u;
+  const uint32_t threads = gridDim.x * 256u;
   float alpha = 0.0f, six_alpha = 0.0f;
   if (!kMx) {
     alpha = amax_dev ? __fdiv_rn(*amax_dev, 2688.0f) : alpha_param;
     six_alpha = __fmul_rn(6.0f, alpha);
     if (alpha_out && blockIdx.x == 0 && threadIdx.x == 0) *alpha_out = alpha;
   }
-  for (uint32_t p0 = blockIdx.x * 8u + (threadIdx.x >> 5); p0 < pieces.total; p0 += warps * kPieces) {
-    float v[kPieces][8];
-    Piece at[kPieces];
+  for (uint32_t q0 = blockIdx.x * 256u + threadIdx.x; q0 < blocks.total; q0 += threads * kAtOnce) {
+    RawBlock<TYPE, N> raw[kAtOnce];
+    uint32_t row[kAtOnce], col[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      at[u] = piece_of(pieces, p0 + u * warps, cols, lane);
-      if (at[u].in)
-        load8<TYPE>(static_cast<const uint8_t*>(src) + (at[u].row * ld + at[u].col) * kSize, v[u]);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t q = q0 + u * threads;
+      split_piece(blocks, q, row[u], col[u]);
+      if (q < blocks.total)
+        raw[u].load(static_cast<const uint8_t*>(src) + (row[u] * ld + static_cast<int64_t>(col[u]) * N) * kSize,
+                    wide);
     }
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      uint32_t m = amax8(v[u]);
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      uint32_t scale, word = 0;
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (q0 + u * threads >= blocks.total) break;
+      const uint32_t m = raw[u].amax();
       const bool finite = m < 0x7F800000u;
+      uint32_t scale, word[N / 8];
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) word[i] = 0;
       if constexpr (kMx) {
         // amax = f * 2^E, f in [1, 2): 6 = 1.5 * 2^2, so e = E - 2 where f <= 1.5, else E - 1
         int e = static_cast<int>(m >> 23) - 127 - 2 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0);
@@ -141,8 +191,9 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e in [-127, 126]
         if (finite) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            word |= cvt_e2m1x2(__fmul_rn(v[u][2 * i], inv), __fmul_rn(v[u][2 * i + 1], inv)) << (8 * i);
+          for (int i = 0; i < N / 2; ++i)
+            word[i / 4] |= cvt_e2m1x2(__fmul_rn(raw[u].value(2 * i), inv), __fmul_rn(raw[u].value(2 * i + 1), inv))
+                           << (8 * (i & 3));
         }
       } else {
         scale = alpha > 0.0f ? cvt_e4m3(__fdiv_rn(__uint_as_float(m), six_alpha)) : 0u;
@@ -150,31 +201,26 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
         if (finite && scale != 0) {
           const float d = __fmul_rn(e4m3_value(scale), alpha);
           const float r = __frcp_rn(d);
-          if (d >= 0x1p-100f && d <= 0x1p100f) {  // no step of the short form leaves FP32's normal range
+          // no step leaves FP32's normal range (a saturated block scale makes large quotients)
+          if (d >= 0x1p-100f && d <= 0x1p100f && __uint_as_float(m) <= d * 0x1p20f) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              word |= cvt_e2m1x2(quotient_for_e2m1(v[u][2 * i], d, r), quotient_for_e2m1(v[u][2 * i + 1], d, r))
-                      << (8 * i);
+            for (int i = 0; i < N / 2; ++i)
+              word[i / 4] |= cvt_e2m1x2(quotient(raw[u].value(2 * i), d, r), quotient(raw[u].value(2 * i + 1), d, r))
+                             << (8 * (i & 3));
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              word |= cvt_e2m1x2(__fdiv_rn(v[u][2 * i], d), __fdiv_rn(v[u][2 * i + 1], d)) << (8 * i);
+            for (int i = 0; i < N / 2; ++i)
+              word[i / 4] |= cvt_e2m1x2(__fdiv_rn(raw[u].value(2 * i), d), __fdiv_rn(raw[u].value(2 * i + 1), d))
+                             << (8 * (i & 3));
           }
         }
       }
-      // four blocks' scales into one word, in the first lane of the four
-      uint32_t four = scale | (__shfl_down_sync(0xffffffffu, scale, kLanes) << 8);
-      four |= __shfl_down_sync(0xffffffffu, four, 2 * kLanes) << 16;
-      if (at[u].in) {
-        *reinterpret_cast<uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)) = word;
-        uint8_t* s = sf + at[u].row * ldsf + at[u].col / (8 * kLanes);
-        const int64_t here = at[u].col & ~static_cast<int64_t>(32 * kLanes - 1);  // first value of the four blocks
-        if (here + 32 * kLanes <= cols) {
-          if (lane % (4 * kLanes) == 0) *reinterpret_cast<uint32_t*>(s) = four;
-        } else if (lane % kLanes == 0) {
-          *s = static_cast<uint8_t>(scale);
-        }
-      }
+      uint8_t* c = codes + row[u] * ldc + static_cast<int64_t>(col[u]) * (N / 2);
+      if constexpr (kMx)
+        *reinterpret_cast<uint4*>(c) = make_uint4(word[0], word[1], word[2], word[3]);
+      else
+        *reinterpret_cast<uint2*>(c) = make_uint2(word[0], word[1]);
+      sf[row[u] * ldsf + col[u]] = static_cast<uint8_t>(scale);
     }
   }
 }
@@ -223,33 +269,42 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A thread turns 32 bytes' worth of values: 16 of 16 bits or 8 of 32.
+template <int OUT>
+constexpr int kOutValues = OUT == kTypeFp32 ? 8 : 16;
+
 template <int FORMAT, int OUT>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                              const uint8_t* __restrict__ sf, int64_t ldsf,
                                                              const float* __restrict__ alpha_dev, Pieces pieces,
-                                                             int64_t cols, void* __restrict__ out, int64_t ldo) {
+                                                             void* __restrict__ out, int64_t ldo, bool wide) {
   constexpr bool kMx = FORMAT == kMxFp4;
-  constexpr int kSize = OUT == kTypeFp32 ? 4 : 2;
+  constexpr int V = kOutValues<OUT>, kAtOnce = 4;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const uint32_t warps = gridDim.x * 8u;
+  const uint32_t threads = gridDim.x * 256u;
   const float alpha = !kMx && alpha_dev ? *alpha_dev : 1.0f;
-  for (uint32_t p0 = blockIdx.x * 8u + (threadIdx.x >> 5); p0 < pieces.total; p0 += warps * kPieces) {
-    uint32_t word[kPieces], scale[kPieces];
-    Piece at[kPieces];
+  for (uint32_t q0 = blockIdx.x * 256u + threadIdx.x; q0 < pieces.total; q0 += threads * kAtOnce) {
+    uint32_t word[kAtOnce][V / 8], scale[kAtOnce], row[kAtOnce], part[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      at[u] = piece_of(pieces, p0 + u * warps, cols, lane);
-      word[u] = scale[u] = 0;
-      if (at[u].in) {
-        word[u] = __ldg(reinterpret_cast<const uint32_t*>(codes + at[u].row * ldc + (at[u].col >> 1)));
-        scale[u] = __ldg(sf + at[u].row * ldsf + at[u].col / (kMx ? 32 : 16));
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t q = q0 + u * threads;
+      split_piece(pieces, q, row[u], part[u]);
+      if (q < pieces.total) {
+        const uint8_t* c = codes + row[u] * ldc + static_cast<int64_t>(part[u]) * (V / 2);
+        if constexpr (V == 16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(c));
+          word[u][0] = w.x;
+          word[u][1] = w.y;
+        } else {
+          word[u][0] = __ldg(reinterpret_cast<const uint32_t*>(c));
+        }
+        scale[u] = __ldg(sf + row[u] * ldsf + static_cast<int64_t>(part[u]) * V / (kMx ? 32 : 16));
       }
     }
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      if (!at[u].in) continue;
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (q0 + u * threads >= pieces.total) break;
       float s;
       if constexpr (kMx) {  // 2^(scale - 127); 0 is the subnormal 2^-127
         s = scale[u] == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(scale[u] << 23);
@@ -257,54 +312,53 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
       } else {
         s = (scale[u] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(scale[u] & 0x7Fu);
       }
-      float v[8];
+      uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 q = e2m1x2_values((word[u] >> (8 * i)) & 0xFFu);
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 q = e2m1x2_values((word[u][i / 4] >> (8 * (i & 3))) & 0xFFu);
         // code times block scale is exact; the tensor scale is one FP32 rounding
-        v[2 * i] = kMx ? __fmul_rn(q.x, s) : __fmul_rn(__fmul_rn(q.x, s), alpha);
-        v[2 * i + 1] = kMx ? __fmul_rn(q.y, s) : __fmul_rn(__fmul_rn(q.y, s), alpha);
-      }
-      uint8_t* p = static_cast<uint8_t*>(out) + (at[u].row * ldo + at[u].col) * kSize;
-      if constexpr (OUT == kTypeFp32) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (OUT == kTypeBf16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            h[i] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            h[i] = *reinterpret_cast<const uint32_t*>(&b);
-          }
+        const float x = kMx ? __fmul_rn(q.x, s) : __fmul_rn(__fmul_rn(q.x, s), alpha);
+        const float y = kMx ? __fmul_rn(q.y, s) : __fmul_rn(__fmul_rn(q.y, s), alpha);
+        if constexpr (OUT == kTypeFp32) {
+          w[2 * i] = __float_as_uint(x);
+          w[2 * i + 1] = __float_as_uint(y);
+        } else if constexpr (OUT == kTypeBf16) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+          const __half2 b = __floats2half2_rn(x, y);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      uint8_t* p = static_cast<uint8_t*>(out) +
+                   (row[u] * ldo + static_cast<int64_t>(part[u]) * V) * (OUT == kTypeFp32 ? 4 : 2);
+      if (wide) {
+        st_global_v8(p, w);
+      } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
   }
 }
 
-// Eight warps to a block; a grid of up to eight blocks an SM, each warp at most four pieces
-// before it repeats.
-unsigned grid_of(const Pieces& p) {
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((int64_t{p.total} + 7) / 8, 148 * 8)));
+// Up to `per_sm` CTAs of 256 threads an SM, each taking `each` pieces at a time.
+unsigned grid_of(const Pieces& p, int each, int per_sm = 8) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((int64_t{p.total} + each - 1) / each, 148 * per_sm)));
 }
 // One launch's share of a matrix: at most kMaxPieces pieces, so that their numbers (and the steps
 // of a loop past the last one) fit 32 bits.
 constexpr int64_t kMaxPieces = int64_t{1} << 30;
-Pieces pieces_of(int64_t rows, int64_t cols) {
-  const int64_t per_row = (cols + kPieceValues - 1) / kPieceValues;
+Pieces pieces_of(int64_t rows, int64_t cols, int values) {
+  const int64_t per_row = (cols + values - 1) / values;
   return Pieces{static_cast<uint32_t>(rows * per_row), static_cast<uint32_t>(per_row),
                 static_cast<uint32_t>(std::min<int64_t>((int64_t{1} << 32) / per_row, 0xFFFFFFFFll))};
 }
 // Calls f(first row, rows, columns) for shares of the matrix, one long row where `flat`.
 template <class F>
-cudaError_t for_shares(int64_t rows, int64_t cols, bool flat, F f) {
-  if (flat && (rows * cols + kPieceValues - 1) / kPieceValues <= kMaxPieces) return f(int64_t{0}, int64_t{1}, rows * cols);
-  const int64_t most = std::max<int64_t>(1, kMaxPieces / ((cols + kPieceValues - 1) / kPieceValues));
+cudaError_t for_shares(int64_t rows, int64_t cols, int values, bool flat, F f) {
+  if (flat && (rows * cols + values - 1) / values <= kMaxPieces) return f(int64_t{0}, int64_t{1}, rows * cols);
+  const int64_t most = std::max<int64_t>(1, kMaxPieces / ((cols + values - 1) / values));
   for (int64_t r = 0; r < rows; r += most) {
     const cudaError_t e = f(r, std::min(most, rows - r), cols);
     if (e != cudaSuccess) return e;
@@ -321,11 +375,13 @@ cudaError_t launch_quantize(int format, const void* src, int64_t ld, int64_t row
                             float* alpha_out, cudaStream_t s) {
   auto k = format == kMxFp4 ? quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_MX> : quantize_fp4_kernel<TYPE, BEAM_MOE_FP4_NV>;
   const bool flat = ld == cols && ldc == cols / 2 && ldsf == cols / (format == kMxFp4 ? 32 : 16);
-  return for_shares(rows, cols, flat, [&](int64_t r, int64_t n, int64_t c) {
-    const Pieces p = pieces_of(n, c);
-    return launch_pdl(k, dim3(grid_of(p)), dim3(256), 0, s,
-                      static_cast<const uint8_t*>(src) + r * ld * (TYPE == kTypeFp32 ? 4 : 2), ld, p, c, alpha,
-                      amax_dev, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha_out);
+  const int values = format == kMxFp4 ? 32 : 16;
+  const bool wide = aligned_to(src, 32) && (rows == 1 || ld * (TYPE == kTypeFp32 ? 4 : 2) % 32 == 0);
+  return for_shares(rows, cols, values, flat, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c, values);
+    return launch_pdl(k, dim3(grid_of(p, 256)), dim3(256), 0, s,
+                      static_cast<const uint8_t*>(src) + r * ld * (TYPE == kTypeFp32 ? 4 : 2), ld, p, alpha,
+                      amax_dev, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha_out, wide);
   });
 }
 
@@ -333,9 +389,9 @@ template <int TYPE>
 cudaError_t launch_amax_finite(const void* src, int64_t ld, int64_t rows, int cols, float* out, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(out, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
-  return for_shares(rows, cols, ld == cols, [&](int64_t r, int64_t n, int64_t c) {
-    const Pieces p = pieces_of(n, c);
-    amax_finite_kernel<TYPE><<<grid_of(p), 256, 0, s>>>(
+  return for_shares(rows, cols, kPieceValues, ld == cols, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c, kPieceValues);
+    amax_finite_kernel<TYPE><<<grid_of(p, 8), 256, 0, s>>>(
         static_cast<const uint8_t*>(src) + r * ld * (TYPE == kTypeFp32 ? 4 : 2), ld, p, c,
         reinterpret_cast<unsigned int*>(out));
     return cudaGetLastError();
@@ -349,10 +405,13 @@ cudaError_t launch_dequantize(int out_type, const uint8_t* codes, int64_t ldc, c
            : out_type == kTypeFp16 ? dequantize_fp4_kernel<FORMAT, kTypeFp16>
                                    : dequantize_fp4_kernel<FORMAT, kTypeFp32>;
   const bool flat = ldo == cols && ldc == cols / 2 && ldsf == cols / (FORMAT == kMxFp4 ? 32 : 16);
-  return for_shares(rows, cols, flat, [&](int64_t r, int64_t n, int64_t c) {
-    const Pieces p = pieces_of(n, c);
-    return launch_pdl(k, dim3(grid_of(p)), dim3(256), 0, s, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha, p, c,
-                      static_cast<void*>(static_cast<uint8_t*>(out) + r * ldo * (out_type == kTypeFp32 ? 4 : 2)), ldo);
+  const int values = out_type == kTypeFp32 ? kOutValues<kTypeFp32> : kOutValues<kTypeBf16>;
+  const bool wide = aligned_to(out, 32) && (rows == 1 || ldo * (out_type == kTypeFp32 ? 4 : 2) % 32 == 0);
+  return for_shares(rows, cols, values, flat, [&](int64_t r, int64_t n, int64_t c) {
+    const Pieces p = pieces_of(n, c, values);
+    return launch_pdl(k, dim3(grid_of(p, 256)), dim3(256), 0, s, codes + r * ldc, ldc, sf + r * ldsf, ldsf, alpha, p,
+                      static_cast<void*>(static_cast<uint8_t*>(out) + r * ldo * (out_type == kTypeFp32 ? 4 : 2)), ldo,
+                      wide);
   });
 }
 
