@@ -17,6 +17,11 @@
 // past a row's last scale are filled with zeros by TMA, so that what lies behind them in memory
 // (a NaN byte times a zero code would be NaN) does not matter.
 //
+// Few tiles.  A decoding step has one row block and few feature tiles (20 for 5120 features), too
+// few pairs to draw weights at the memory's rate.  Then a cluster of S pairs shares a tile: each
+// multiplies its stretch of K, and the first pair adds the others' sums, received in its shared
+// memory, in their order (the result does not depend on timing).
+//
 // A CTA (768 threads): warp 0 loads (a ring of 5 stages of 38 KB: 256 K values of 128 B rows
 // and of half of the A rows, and their scales), warp 1 of the leading CTA issues the MMAs, warp
 // 3 owns TMEM, warps 4..7 move scales, warps 8..23 store results.  One accumulator of 256
@@ -57,6 +62,7 @@ constexpr int F4_THREADS = 32 * (F4_FIRST_EPI + F4_EPI_WARPS);
 struct Fp4Args {
   int m, n, k;             // D is [m][n]
   int blocks, height;      // A's rows in equal blocks, their height a multiple of 32 up to 256
+  int split;               // pairs that share a tile (1: each pair its own tiles)
   const float* alpha_a;    // tensor scales, or nullptr
   const float* alpha_b;
   void* out;
@@ -135,8 +141,8 @@ struct Fp4Maps {
   CUtensorMap m_codes, n_codes, m_sf, n_sf;
 };
 
-template <int FORMAT, int OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
+template <int FORMAT, int OUT, bool kSplit>
+__global__ void __launch_bounds__(F4_THREADS, 1)
     gemm_fp4_kernel(const Fp4Args args, const __grid_constant__ Fp4Maps maps) {
   constexpr bool kMx = FORMAT == BEAM_MOE_FP4_MX;
   extern __shared__ uint8_t smem_raw[];
@@ -144,7 +150,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
   Fp4Tail* tail = reinterpret_cast<Fp4Tail*>(smem + F4_STAGES * F4_STAGE);
   volatile int* abort_flag = &tail->abort_flag;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_cta_rank();
+  const uint32_t cluster_rank = cluster_cta_rank();
+  const uint32_t rank = cluster_rank & 1;                        // in the pair
+  const uint32_t first = kSplit ? cluster_rank & ~1u : 0u;       // the pair's leading CTA
+  const int pair = kSplit ? static_cast<int>(cluster_rank >> 1) : 0;
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&maps.m_codes);
@@ -173,8 +182,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
   pdl_trigger();
   const uint32_t tmem = tail->tmem_base;
   const int total = args.blocks * ((args.n + F4_TILE - 1) / F4_TILE);
-  const int first_tile = blockIdx.x >> 1, tile_stride = gridDim.x >> 1;
-  const int steps = (args.k + F4_BK - 1) / F4_BK;
+  const int all_steps = (args.k + F4_BK - 1) / F4_BK;
+  // this pair's tiles and K steps: every tile_stride-th tile, or one tile and a share of its steps
+  const int first_tile = kSplit ? static_cast<int>(blockIdx.x) / (2 * args.split) : blockIdx.x >> 1;
+  const int tile_stride = kSplit ? total : gridDim.x >> 1;
+  const int step0 = kSplit ? all_steps * pair / args.split : 0;
+  const int step1 = kSplit ? all_steps * (pair + 1) / args.split : all_steps;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -186,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
       const Fp4Tile t = fp4_tile(args, id);
       const int half = t.n >> 1;
       const int f0 = t.f0 + static_cast<int>(rank) * 128, r0 = t.r0 + static_cast<int>(rank) * half;
-      for (int i = 0; i < steps; ++i) {
+      for (int i = step0; i < step1; ++i) {
         ok = __all_sync(0xffffffffu, pair_wait(&tail->empty[stage], phase ^ 1, abort_flag));
         if (!ok) break;
         if (elect_one()) {
@@ -227,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n >> 3) << 17);
-        for (int i = 0; i < steps; ++i) {
+        for (int i = step0; i < step1; ++i) {
           if (!ready) {
             ok = __all_sync(0xffffffffu, pair_wait(&tail->sf_full[stage], phase, abort_flag));
             if (!ok) break;
@@ -248,19 +261,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
             const int group = kMx ? j >> 1 : j;
             const uint32_t half = kMx ? static_cast<uint32_t>(j & 1) * 2 : 0u;
             tc_mma_fp4_pair<FORMAT>(tmem, da + j * 2, db + j * 2, idesc | (half << 29) | (half << 4), sf + group * 4,
-                                    sf + F4_SF_N + group * 8, (i | j) != 0 ? 1u : 0u, leader);
+                                    sf + F4_SF_N + group * 8, ((i - step0) | j) != 0 ? 1u : 0u, leader);
           }
-          tc_commit_pair(&tail->empty[stage], leader);
+          tc_commit_pair(&tail->empty[stage], leader, first);
           stage = next;
           phase = next_phase;
           ready = __all_sync(0xffffffffu, next_ready);
         }
         if (!ok) break;
-        tc_commit_pair(&tail->acc_full, leader);
+        tc_commit_pair(&tail->acc_full, leader, first);
         acc_phase ^= 1;
       }
       if (!ok) {  // nothing may read shared memory or write TMEM after the CTAs are gone
-        tc_commit_pair(&tail->drain, leader);
+        tc_commit_pair(&tail->drain, leader, first);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&tail->drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
@@ -274,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
     bool ok = true;
     for (int id = first_tile; id < total && ok; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
-      for (int i = 0; i < steps; ++i) {
+      for (int i = step0; i < step1; ++i) {
         ok = __all_sync(0xffffffffu, pair_wait(&tail->full[stage], phase, abort_flag));
         if (!ok) break;
         const uint8_t* sm = smem + stage * F4_STAGE + F4_OFF_SFM + lane * 16;
@@ -325,10 +338,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->sf_full[stage], 0));
+        if (lane == 0) mbar_arrive_at(map_to_cta(&tail->sf_full[stage], first));
         if (++stage == F4_STAGES) {
           stage = 0;
           phase ^= 1;
+        }
+      }
+    }
+  } else if (kSplit && warp >= F4_FIRST_EPI) {
+    // ------------------------------------------------------------ results of a shared tile
+    const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;
+    const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
+    const Fp4Tile t = fp4_tile(args, first_tile);
+    const bool ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_full, 0, abort_flag));
+    tc_fence_after();
+    const int rows = t.r_end - t.r0, slot = quarter * 32 + lane;
+    const int f = t.f0 + static_cast<int>(rank) * 128 + slot;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // The sums [pair - 1][row][128 features] of the other pairs go into the ring of the first
+    // pair's CTAs, once no pair's MMAs read it any more.  8 columns at a time, every fourth
+    // stretch of 8 to a warp.
+    cluster_sync();
+    if (ok && pair > 0) {
+      const uint32_t to = map_to_cta(smem, rank) + static_cast<uint32_t>((pair - 1) * t.n * 128 + slot) * 4;
+      for (int c = part * 8; c < rows; c += 32) {
+        uint32_t v[8];
+        tmem_ld_32x32b_x8(from + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < rows) st_cluster_f32(to + static_cast<uint32_t>(c + j) * 512, __uint_as_float(v[j]));
+      }
+    }
+    cluster_sync();
+    if (ok && pair == 0) {
+      const float* got = reinterpret_cast<const float*>(smem) + slot;
+      for (int c = part * 8; c < rows; c += 32) {
+        uint32_t v[8];
+        tmem_ld_32x32b_x8(from + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (c + j >= rows || f >= args.n) continue;
+          float sum = __uint_as_float(v[j]);
+          for (int q = 0; q < args.split - 1; ++q) sum += got[(q * t.n + c + j) * 128];
+          const int64_t to = static_cast<int64_t>(t.r0 + c + j) * args.ldo + f;
+          if constexpr (OUT == kTypeFp32)
+            static_cast<float*>(args.out)[to] = sum * scale;
+          else
+            static_cast<uint16_t*>(args.out)[to] = static_cast<uint16_t>(pack_pair<OUT>(sum * scale, 0.0f));
         }
       }
     }
@@ -351,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty, 0));
+      if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty, first));
       // a lane holds feature f of 32 consecutive rows, twice
       const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
 #pragma unroll
@@ -386,6 +444,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F4_THREADS, 1)
     }
   }
   __syncwarp();
+  if (kSplit && warp < F4_FIRST_EPI) {  // the storing warps exchange sums between these
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal or read it
   tc_fence_after();
@@ -407,19 +469,31 @@ bool make_bytes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int FORMAT, int OUT, bool kSplit>
+cudaError_t launch_fp4_as(const Fp4Args& a, const Fp4Maps& maps, unsigned grid, unsigned cluster, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<FORMAT, OUT, kSplit>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFp4Smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl_clusters(gemm_fp4_kernel<FORMAT, OUT, kSplit>, grid, cluster, F4_THREADS, kFp4Smem, s, a, maps);
+}
+
 template <int FORMAT, int OUT>
-cudaError_t launch_fp4(const Fp4Args& a, const Fp4Maps& maps, cudaStream_t s) {
+cudaError_t launch_fp4(Fp4Args a, const Fp4Maps& maps, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(gemm_fp4_kernel<FORMAT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kFp4Smem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.blocks) * ((a.n + F4_TILE - 1) / F4_TILE);
-  const int64_t pairs = std::min<int64_t>(sms / 2, tiles);
-  return launch_pdl(gemm_fp4_kernel<FORMAT, OUT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(F4_THREADS), kFp4Smem,
-                    s, a, maps);
+  // As many pairs to a tile as leave no SM idle, each with two K steps at least, their sums fitting
+  // the ring, in clusters of up to eight CTAs.
+  const int64_t steps = (a.k + F4_BK - 1) / F4_BK;
+  const int64_t fit = 1 + F4_STAGES * F4_STAGE / (static_cast<int64_t>(a.height) * 128 * 4);
+  a.split = static_cast<int>(std::min({int64_t{4}, sms / 2 / tiles, steps / 2, fit}));
+  if (a.split > 1)
+    return launch_fp4_as<FORMAT, OUT, true>(a, maps, static_cast<unsigned>(tiles * 2 * a.split),
+                                            static_cast<unsigned>(2 * a.split), s);
+  a.split = 1;
+  return launch_fp4_as<FORMAT, OUT, false>(a, maps, static_cast<unsigned>(2 * std::min<int64_t>(sms / 2, tiles)), 2, s);
 }
 
 template <int FORMAT>
@@ -468,7 +542,7 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
       !make_bytes_map(&maps.n_sf, a_sf, scales, m, lda_sf, 16, height, false))
     return BEAM_MOE_ERR_INVALID_ARG;
   // MXFP4 has no tensor scale
-  const Fp4Args args{m, n, k, blocks, height, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
+  const Fp4Args args{m, n, k, blocks, height, 1, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mx ? launch_format<BEAM_MOE_FP4_MX>(out_type, args, maps, s)
                            : launch_format<BEAM_MOE_FP4_NV>(out_type, args, maps, s);
