@@ -19,7 +19,7 @@
 //
 // Few tiles.  A decoding step has one row block and few feature tiles (20 for 5120 features), too
 // few pairs to draw weights at the memory's rate.  Then a cluster of S pairs shares a tile: each
-// multiplies its stretch of K, and the first pair adds the others' sums, received in its shared
+// multiplies its stretch of K, and the first pair adds the others' sums, copied into its shared
 // memory, in their order (the result does not depend on timing).
 //
 // A CTA (768 threads): warp 0 loads (a ring of 5 stages of 38 KB: 256 K values of 128 B rows
@@ -56,6 +56,8 @@ constexpr int F4_SF_COL = 256;                  // TMEM columns of the stages' s
 constexpr int F4_SF_STAGE = 48;                 // M: 4 columns per K group, then N: 8 per K group
 constexpr int F4_SF_N = 16;
 static_assert(F4_SF_COL + F4_STAGES * F4_SF_STAGE <= 512, "scales fit in TMEM");
+constexpr int F4_MAX_SPLIT = 4;                 // pairs that share a tile
+constexpr int F4_SUM_ROWS = 64;                 // rows of sums that a shared tile's first pair can receive
 constexpr int F4_FIRST_SF = 4, F4_FIRST_EPI = 8, F4_EPI_WARPS = 16;
 constexpr int F4_THREADS = 32 * (F4_FIRST_EPI + F4_EPI_WARPS);
 
@@ -76,8 +78,10 @@ struct __align__(16) Fp4Tail {
   uint64_t acc_full;
   uint64_t acc_empty;            // leader
   uint64_t drain;
+  uint64_t sums_full;            // shared tiles: the other pairs' sums have come
   uint32_t tmem_base;
   int abort_flag;
+  alignas(16) float sums[F4_SUM_ROWS * 128];
 };
 constexpr size_t kFp4Smem = static_cast<size_t>(F4_STAGES) * F4_STAGE + sizeof(Fp4Tail) + 1024;
 static_assert(kFp4Smem <= 227 * 1024, "shared memory of one CTA");
@@ -168,6 +172,9 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     mbar_init(&tail->acc_full, 1);
     mbar_init(&tail->acc_empty, 2 * F4_EPI_WARPS);
     mbar_init(&tail->drain, 1);
+    mbar_init(&tail->sums_full, 1);
+    if (kSplit && pair == 0)
+      mbar_arrive_expect_tx(&tail->sums_full, static_cast<uint32_t>((args.split - 1) * args.m) * 512);
     tail->abort_flag = 0;
     fence_mbar_init();
   }
@@ -355,33 +362,36 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     const int rows = t.r_end - t.r0, slot = quarter * 32 + lane;
     const int f = t.f0 + static_cast<int>(rank) * 128 + slot;
     const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    // The sums [pair - 1][row][128 features] of the other pairs go into the ring of the first
-    // pair's CTAs, once no pair's MMAs read it any more.  8 columns at a time, every fourth
-    // stretch of 8 to a warp.
-    cluster_sync();
-    if (ok && pair > 0) {
-      const uint32_t to = map_to_cta(smem, rank) + static_cast<uint32_t>((pair - 1) * t.n * 128 + slot) * 4;
-      for (int c = part * 8; c < rows; c += 32) {
-        uint32_t v[8];
-        tmem_ld_32x32b_x8(from + c, v);
+    // 2 columns at a time, every fourth stretch of 2 to a warp
+    if (pair > 0) {
+      // this CTA's sums [row][128 features] to the start of its ring (its MMAs are done), and from
+      // there in one copy to the first pair's CTA; plain remote stores took 0.2 us a row
+      float* mine = reinterpret_cast<float*>(smem) + slot;
+      for (int c = part * 2; ok && c < rows; c += 8) {
+        uint32_t v[2];
+        tmem_ld_32x32b_x2(from + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j < rows) st_cluster_f32(to + static_cast<uint32_t>(c + j) * 512, __uint_as_float(v[j]));
+        for (int j = 0; j < 2; ++j)
+          if (c + j < rows) mine[(c + j) * 128] = __uint_as_float(v[j]);
       }
-    }
-    cluster_sync();
-    if (ok && pair == 0) {
-      const float* got = reinterpret_cast<const float*>(smem) + slot;
-      for (int c = part * 8; c < rows; c += 32) {
-        uint32_t v[8];
-        tmem_ld_32x32b_x8(from + c, v);
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * F4_EPI_WARPS) : "memory");
+      if (ok && warp == F4_FIRST_EPI && lane == 0)
+        bulk_copy_to_cta(map_to_cta(tail->sums + (pair - 1) * rows * 128, rank), smem, static_cast<uint32_t>(rows) * 512,
+                         map_to_cta(&tail->sums_full, rank));
+    } else if (ok && __all_sync(0xffffffffu, pair_wait(&tail->sums_full, 0, abort_flag))) {
+      for (int c = part * 2; c < rows; c += 8) {
+        uint32_t v[2];
+        tmem_ld_32x32b_x2(from + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 2; ++j) {
           if (c + j >= rows || f >= args.n) continue;
           float sum = __uint_as_float(v[j]);
-          for (int q = 0; q < args.split - 1; ++q) sum += got[(q * t.n + c + j) * 128];
+#pragma unroll
+          for (int q = 0; q < F4_MAX_SPLIT - 1; ++q)
+            if (q < args.split - 1) sum += tail->sums[(q * rows + c + j) * 128 + slot];
           const int64_t to = static_cast<int64_t>(t.r0 + c + j) * args.ldo + f;
           if constexpr (OUT == kTypeFp32)
             static_cast<float*>(args.out)[to] = sum * scale;
@@ -444,10 +454,6 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     }
   }
   __syncwarp();
-  if (kSplit && warp < F4_FIRST_EPI) {  // the storing warps exchange sums between these
-    cluster_sync();
-    cluster_sync();
-  }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal or read it
   tc_fence_after();
@@ -484,11 +490,12 @@ cudaError_t launch_fp4(Fp4Args a, const Fp4Maps& maps, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.blocks) * ((a.n + F4_TILE - 1) / F4_TILE);
-  // As many pairs to a tile as leave no SM idle, each with two K steps at least, their sums fitting
-  // the ring, in clusters of up to eight CTAs.
+  // As many pairs to a tile of one row block as leave no SM idle, as far as the first can receive
+  // their sums, in clusters of up to eight CTAs, and each with a ring's worth of K steps at least:
+  // the exchange takes as long as those.
   const int64_t steps = (a.k + F4_BK - 1) / F4_BK;
-  const int64_t fit = 1 + F4_STAGES * F4_STAGE / (static_cast<int64_t>(a.height) * 128 * 4);
-  a.split = static_cast<int>(std::min({int64_t{4}, sms / 2 / tiles, steps / 2, fit}));
+  const int64_t fit = a.blocks == 1 ? 1 + F4_SUM_ROWS / a.m : 1;
+  a.split = static_cast<int>(std::min({int64_t{F4_MAX_SPLIT}, sms / 2 / tiles, steps / F4_STAGES, fit}));
   if (a.split > 1)
     return launch_fp4_as<FORMAT, OUT, true>(a, maps, static_cast<unsigned>(tiles * 2 * a.split),
                                             static_cast<unsigned>(2 * a.split), s);

@@ -155,7 +155,10 @@ def test_bytes_between_the_rows_stay(bm):
 
 
 PRODUCTS = [(1, 1, 32), (1, 256, 256), (3, 40, 64), (33, 129, 288), (64, 512, 512), (257, 300, 96), (160, 264, 1056),
-            (1, 5120, 1536), (700, 520, 1312), (2100, 136, 224)]
+            (1, 5120, 1536), (700, 520, 1312), (2100, 136, 224),
+            # a tile shared by several pairs: few tiles, long sums, up to 64 rows
+            (1, 300, 2592), (5, 8192, 2560), (20, 520, 5120), (21, 1000, 5120), (32, 129, 5120), (64, 256, 2816),
+            (65, 256, 2816)]
 
 
 @pytest.mark.parametrize("out", [BF16, FP16, FP32])
