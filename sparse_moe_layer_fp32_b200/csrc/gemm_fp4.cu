@@ -81,8 +81,9 @@ struct __align__(16) Fp4Tail {
   uint64_t sums_full;            // shared tiles: the other pairs' sums have come
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float sums[F4_SUM_ROWS * 128];
+  alignas(16) float sums[F4_SUM_ROWS * 128];  // shared tiles: received sums; else results on their way out
 };
+static_assert(sizeof(Fp4Tail::sums) >= 4 * 8192, "8 KB for each four storing warps");
 constexpr size_t kFp4Smem = static_cast<size_t>(F4_STAGES) * F4_STAGE + sizeof(Fp4Tail) + 1024;
 static_assert(kFp4Smem <= 227 * 1024, "shared memory of one CTA");
 
@@ -126,17 +127,6 @@ __device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc,
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(leader)
         : "memory");
-}
-
-template <int OUT>
-__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
-  if constexpr (OUT == kTypeBf16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
 }
 
 // Boxes: 128 rows of B; half a block's and a whole block's rows of A (the last block is shorter:
@@ -404,7 +394,8 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     // ------------------------------------------------------------ results
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;  // 64 columns of a lane quarter
     const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
-    const bool pairs = OUT != kTypeFp32 && ((args.n | args.ldo) & 1) == 0;
+    const bool whole_rows =
+        OUT != kTypeFp32 && ((args.n | args.ldo) & 7) == 0 && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0;
     uint32_t acc_phase = 0;
     for (int id = first_tile; id < total; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
@@ -431,18 +422,11 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (row + j < t.r_end && f < args.n) p[j * args.ldo] = __uint_as_float(v[h][j]) * scale;
-        } else if (pairs) {
-          // neighbouring lanes trade values, so that each stores two features of one row
-          const int odd = lane & 1;
-          uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row + odd) * args.ldo + (f - odd);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float mine = __uint_as_float(odd ? v[h][j + 1] : v[h][j]) * scale;
-            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[h][j] : v[h][j + 1], 1)) * scale;
-            const uint32_t w = odd ? pack_pair<OUT>(other, mine) : pack_pair<OUT>(mine, other);
-            if (row + j + odd < t.r_end && f < args.n) *reinterpret_cast<uint32_t*>(p + j * args.ldo) = w;
-          }
-        } else {  // rows that start on odd elements: one value at a time
+        } else if (whole_rows) {
+          store_turned<OUT>(v[h], scale, reinterpret_cast<uint8_t*>(tail->sums) + part * 8192, 1 + part, quarter, lane,
+                            static_cast<uint16_t*>(args.out), args.ldo, row, t.r_end,
+                            t.f0 + static_cast<int>(rank) * 128, args.n);
+        } else {  // rows off 16-byte boundaries: one value at a time
           uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row) * args.ldo + f;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

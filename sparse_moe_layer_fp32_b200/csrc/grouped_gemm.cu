@@ -78,7 +78,9 @@ struct GroupedArgs {
 };
 
 struct __align__(16) GroupedTail {
-  uint8_t turn[GG_EPI_WARPS][32 * 64];  // wgrad: 32 rows x 64 bytes of results of each storing warp
+  // results on their way out: wgrad 32 rows x 64 bytes of each storing warp, else 32 rows x 128
+  // features of each four
+  uint8_t turn[GG_EPI_WARPS * 2048];
   uint64_t full[GG_STAGES];       // leader: both CTAs' halves have landed
   uint64_t empty[GG_STAGES];
   uint64_t landed[GG_STAGES];     // wgrad: this CTA's half of a ragged stage has landed
@@ -139,17 +141,6 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedArgs& a, const 
   t.n = max(32, (t.n_end - t.n0 + 31) & ~31);
   t.steps = (a.kdim + GG_BK - 1) / GG_BK;
   return t;
-}
-
-template <int OUT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (OUT == kTypeBf16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
 }
 
 template <int MODE, int OUT>
@@ -409,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
           // longer than their multiplication (290 against 191 us with no stores at all).
           constexpr int kBytes = OUT == kTypeFp32 ? 4 : 2;
           constexpr int kCols = 64 / kBytes;  // columns of one pass: 64 bytes of each row
-          uint8_t* tile = tail->turn[w];
+          uint8_t* tile = tail->turn + w * 2048;
           const int sub = lane >> 2, part = lane & 3;
 #pragma unroll
           for (int h = 0; h < 32 / kCols; ++h) {
@@ -422,10 +413,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
                 q = make_uint4(f[0], f[1], f[2], f[3]);
               } else {
                 const uint32_t* f = v + 8 * j;
-                q.x = pack2<OUT>(__uint_as_float(f[0]), __uint_as_float(f[1]));
-                q.y = pack2<OUT>(__uint_as_float(f[2]), __uint_as_float(f[3]));
-                q.z = pack2<OUT>(__uint_as_float(f[4]), __uint_as_float(f[5]));
-                q.w = pack2<OUT>(__uint_as_float(f[6]), __uint_as_float(f[7]));
+                q.x = pack_pair<OUT>(__uint_as_float(f[0]), __uint_as_float(f[1]));
+                q.y = pack_pair<OUT>(__uint_as_float(f[2]), __uint_as_float(f[3]));
+                q.z = pack_pair<OUT>(__uint_as_float(f[4]), __uint_as_float(f[5]));
+                q.w = pack_pair<OUT>(__uint_as_float(f[6]), __uint_as_float(f[7]));
               }
               *reinterpret_cast<uint4*>(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = q;
             }
@@ -449,16 +440,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             for (int j = 0; j < 32; ++j)
               if (row + j < t.n_end && m < args.m) p[j * args.ldo] = __uint_as_float(v[j]);
           } else {
-            // neighbouring lanes trade values, so that each stores two features of one row
-            const int odd = lane & 1;
-            uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row + odd) * args.ldo + (m - odd);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
-              const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1));
-              const uint32_t h = odd ? pack2<OUT>(other, mine) : pack2<OUT>(mine, other);
-              if (row + j + odd < t.n_end && m < args.m) *reinterpret_cast<uint32_t*>(p + j * args.ldo) = h;
-            }
+            store_turned<OUT>(v, 1.0f, tail->turn + side * 8192, 1 + side, quarter, lane,
+                              static_cast<uint16_t*>(args.out), args.ldo, row, t.n_end,
+                              t.m0 + static_cast<int>(rank) * 128, args.m);
           }
         }
       }
