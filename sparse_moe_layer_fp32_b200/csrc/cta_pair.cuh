@@ -222,9 +222,8 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
 // four warps (one per lane quarter) hold 32 columns of this CTA's 128 features; v: this lane's
 // feature in rows row0 .. row0 + 31.  Neighbouring lanes trade values so that each has two
 // features of one row; the 32 x 128 values are turned in 8 KB of shared memory and leave as whole
-// 256-byte rows.  Stored straight from the lanes, in pieces of 64 bytes, a tile's results held up
-// the loads of the next: 180 us for a 16384 x 5120 x 5120 product of 4-bit operands, 148 without
-// any stores.  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
+// 256-byte rows (against 64-byte pieces straight from the lanes: 1% less time for the grouped
+// products; the 4-bit product, which shared memory bounds, is 2 to 4% faster without).  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
 // barrier: a named barrier of these four warps.
 template <int OUT>
 __device__ __forceinline__ void store_turned(const uint32_t (&v)[32], float scale, uint8_t* turn, int barrier, int quarter,

@@ -81,9 +81,8 @@ struct __align__(16) Fp4Tail {
   uint64_t sums_full;            // shared tiles: the other pairs' sums have come
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float sums[F4_SUM_ROWS * 128];  // shared tiles: received sums; else results on their way out
+  alignas(16) float sums[F4_SUM_ROWS * 128];  // shared tiles: received sums
 };
-static_assert(sizeof(Fp4Tail::sums) >= 4 * 8192, "8 KB for each four storing warps");
 constexpr size_t kFp4Smem = static_cast<size_t>(F4_STAGES) * F4_STAGE + sizeof(Fp4Tail) + 1024;
 static_assert(kFp4Smem <= 227 * 1024, "shared memory of one CTA");
 
@@ -191,7 +190,8 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t bytes = F4_CODES + 128 * 16 + static_cast<uint32_t>(args.height) * (128 / 2 + 16);
+    const uint32_t code_bytes = F4_CODES + static_cast<uint32_t>(args.height) * (128 / 2);
+    const uint32_t sf_bytes = 128 * 16 + static_cast<uint32_t>(args.height) * 16;
     for (int id = first_tile; id < total && ok; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
       const int half = t.n >> 1;
@@ -202,13 +202,17 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
         if (elect_one()) {
           uint8_t* s = smem + stage * F4_STAGE;
           uint64_t* bar = &tail->full[stage];
-          // 16 scale bytes of a row: this K step's (NVFP4), or those of an even step and the next
-          const int sx = kMx ? (i >> 1) * 16 : i * 16;
-          mbar_arrive_expect_tx(bar, bytes);
+          // 16 scale bytes of a row: this K step's (NVFP4), or those of an even step and the next,
+          // which finds them in the scale warps' registers
+          const bool scales = !kMx || (i & 1) == 0 || i == step0;
+          mbar_arrive_expect_tx(bar, code_bytes + (scales ? sf_bytes : 0));
           tma_load_2d(s, &maps.m_codes, bar, i * 128, f0);
-          tma_load_2d(s + F4_OFF_SFM, &maps.m_sf, bar, sx, f0);
           tma_load_2d(s + F4_OFF_N, &maps.n_codes, bar, i * 128, r0);
-          tma_load_2d(s + F4_OFF_SFN, &maps.n_sf, bar, sx, t.r0);
+          if (scales) {
+            const int sx = kMx ? (i >> 1) * 16 : i * 16;
+            tma_load_2d(s + F4_OFF_SFM, &maps.m_sf, bar, sx, f0);
+            tma_load_2d(s + F4_OFF_SFN, &maps.n_sf, bar, sx, t.r0);
+          }
         }
         __syncwarp();
         if (++stage == F4_STAGES) {
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int id = first_tile; id < total && ok; id += tile_stride) {
-      const Fp4Tile t = fp4_tile(args, id);
+      uint4 held[12];  // MXFP4: the scales of an even step and the next
       for (int i = step0; i < step1; ++i) {
         ok = __all_sync(0xffffffffu, pair_wait(&tail->full[stage], phase, abort_flag));
         if (!ok) break;
@@ -293,21 +297,25 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
         // lane l takes rows l, l + 32, ...: row l + 32 q goes to column q (and 4 more for N rows
         // from 128 on) of its K group
         if constexpr (kMx) {
-          const int at = (i & 1) * 8;
+          if ((i & 1) == 0 || i == step0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) held[q] = *reinterpret_cast<const uint4*>(sm + q * 512);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) held[4 + q] = *reinterpret_cast<const uint4*>(sn + q * 512);
+          }
+          const bool upper = (i & 1) != 0;
           uint32_t r[8];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sm + q * 512 + at);
-            r[q] = v.x;
-            r[4 + q] = v.y;
+            r[q] = upper ? held[q].z : held[q].x;
+            r[4 + q] = upper ? held[q].w : held[q].y;
           }
           tmem_st_32x32b_x8(col, r);
           uint32_t w[16];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sn + q * 512 + at);
-            w[q] = v.x;
-            w[8 + q] = v.y;
+            w[q] = upper ? held[4 + q].z : held[4 + q].x;
+            w[8 + q] = upper ? held[4 + q].w : held[4 + q].y;
           }
           tmem_st_32x32b_x16(col + F4_SF_N, w);
         } else {
@@ -394,8 +402,9 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     // ------------------------------------------------------------ results
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;  // 64 columns of a lane quarter
     const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
-    const bool whole_rows =
-        OUT != kTypeFp32 && ((args.n | args.ldo) & 7) == 0 && (reinterpret_cast<uintptr_t>(args.out) & 15) == 0;
+    // two features of a row go as one 4-byte store where every row starts on 4 bytes
+    const bool pairs =
+        ((args.n | args.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(args.out) & 3) == 0;
     uint32_t acc_phase = 0;
     for (int id = first_tile; id < total; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
@@ -422,11 +431,18 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (row + j < t.r_end && f < args.n) p[j * args.ldo] = __uint_as_float(v[h][j]) * scale;
-        } else if (whole_rows) {
-          store_turned<OUT>(v[h], scale, reinterpret_cast<uint8_t*>(tail->sums) + part * 8192, 1 + part, quarter, lane,
-                            static_cast<uint16_t*>(args.out), args.ldo, row, t.r_end,
-                            t.f0 + static_cast<int>(rank) * 128, args.n);
-        } else {  // rows off 16-byte boundaries: one value at a time
+        } else if (pairs) {
+          // neighbouring lanes trade values, so that each stores two features of one row
+          const int odd = lane & 1;
+          uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row + odd) * args.ldo + (f - odd);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float mine = __uint_as_float(odd ? v[h][j + 1] : v[h][j]) * scale;
+            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[h][j] : v[h][j + 1], 1)) * scale;
+            const uint32_t w = odd ? pack_pair<OUT>(other, mine) : pack_pair<OUT>(mine, other);
+            if (row + j + odd < t.r_end && f < args.n) *reinterpret_cast<uint32_t*>(p + j * args.ldo) = w;
+          }
+        } else {  // rows that may start on odd elements: one value at a time
           uint16_t* p = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(row) * args.ldo + f;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {

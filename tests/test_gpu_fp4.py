@@ -128,6 +128,37 @@ def test_extreme_magnitudes(bm, fmt):
     np.testing.assert_array_equal(_norm(codes.cpu().numpy()), _norm(rc))
 
 
+def test_quotients_near_every_e2m1_border(bm):
+    # NVFP4 divides by scale * alpha; quotients on a border between two codes and a few units in
+    # the last place around it, for many divisors, where the code hangs on the last bit of the
+    # IEEE quotient; and the same through BF16 and FP16, whose quotients meet borders exactly
+    rng = np.random.default_rng(77)
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    for alpha in (np.float32(1.0), np.float32(0.37), np.float32(1e-3), np.float32(3.1e-5), np.float32(2.0 ** -9),
+                  np.float32(3e-31), np.float32(2e31)):
+        rows = []
+        for code in rng.choice(np.arange(8, 127), 40, replace=False):
+            d = np.float32(nvfp4.e4m3_decode(np.uint8(code)) * alpha)
+            top = np.float32(np.float32(6.0) * d)  # gives the block this scale
+            for b in borders:
+                base = np.float32(b * d)
+                near = [base]
+                for to in (np.float32(0), np.float32(np.inf)):
+                    v = base
+                    for _ in range(7):
+                        v = np.nextafter(v, to)
+                        near.append(v)
+                rows.append(np.array([top, *near], np.float32) * np.where(rng.random(16) < 0.5, -1, 1))
+        v = np.stack(rows).reshape(-1, 32).astype(np.float32)
+        for kind in (FP32, BF16, FP16):
+            x = torch.from_numpy(v).cuda().to(kind)
+            x = torch.where(torch.isfinite(x), x, 0)
+            codes, sf, _ = bm.beam_moe_quantize_fp4(x, "nvfp4", alpha=float(alpha))
+            rc, rs = _oracle(x, "nvfp4", alpha)
+            np.testing.assert_array_equal(sf.cpu().numpy(), rs)
+            np.testing.assert_array_equal(_norm(codes.cpu().numpy()), _norm(rc))
+
+
 def test_strides_of_the_quantiser(bm):
     whole = _draw((50, 320), BF16, 7)
     x = whole[:, 32:256]
@@ -192,7 +223,7 @@ def test_product_strides_and_padding(bm, fmt):
                                 alpha_a=ops[0][2], alpha_b=ops[1][2])
     va, vb = (_values(c, s, fmt, None if al is None else al.item()) for c, s, al in ops)
     _close(want, va @ vb.t(), va.abs() @ vb.abs().t(), k)
-    for width, at in ((n + 16, 8), (n + 3, 1)):
+    for width, at in ((n + 16, 8), (n + 3, 1), (n + 4, 1), (n + 2, 2)):
         whole = torch.full((m, width), 5.0, dtype=BF16, device="cuda")
         bm.beam_moe_gemm_fp4(ops[0][0], ops[0][1], ops[1][0], ops[1][1], fmt, alpha_a=ops[0][2], alpha_b=ops[1][2],
                              out=whole[:, at:at + n])

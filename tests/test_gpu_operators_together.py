@@ -1,0 +1,86 @@
+"""The operators in a row, as a program uses them: a BF16 mixture-of-experts layer trained through
+the routing and the grouped products, and 4-bit projections one after another."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def bm():
+    import sparse_moe_layer_fp32_b200 as m
+    yield m
+    m.beam_moe_check_operators()
+
+
+def _draw(shape, kind, seed, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(kind)
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 300])
+def test_a_layers_training_step(bm, tokens):
+    hidden, experts, top_k, inter = 256, 16, 2, 128
+    x, w_r = _draw((tokens, hidden), BF16, 1), _draw((experts, hidden), FP32, 2, hidden ** -0.5)
+    w_gu, w_d = _draw((experts, 2 * inter, hidden), BF16, 3, 0.06), _draw((experts, hidden, inter), BF16, 4, 0.09)
+    dout = _draw((tokens, hidden), BF16, 5)
+
+    ids, weight = bm.beam_moe_route(x, w_r, top_k)
+    flat = ids.flatten().long()
+    order = torch.argsort(flat, stable=True)  # slots sorted by expert
+    offsets = torch.cat([flat.new_zeros(1), torch.bincount(flat, minlength=experts).cumsum(0)]).int()
+    token, slot_w = order // top_k, weight.flatten()[order][:, None]
+
+    # forward
+    rows = x[token]
+    gu = bm.beam_moe_grouped_gemm(rows, w_gu, offsets)
+    g, u = gu.float().chunk(2, 1)
+    h = (torch.nn.functional.silu(g) * u).to(BF16)
+    y = bm.beam_moe_grouped_gemm(h, w_d, offsets)
+    out = torch.zeros(tokens, hidden, device="cuda").index_add_(0, token, y.float() * slot_w)
+    # backward
+    dy = (dout[token].float() * slot_w).to(BF16)
+    dw_d = bm.beam_moe_grouped_gemm_wgrad(dy, h, offsets, out_dtype=FP32)
+    dh = bm.beam_moe_grouped_gemm_dgrad(dy, w_d, offsets).float()
+    s = torch.sigmoid(g)
+    dgu = torch.cat([dh * u * s * (1 + g * (1 - s)), dh * g * s], 1).to(BF16)
+    dw_gu = bm.beam_moe_grouped_gemm_wgrad(dgu, rows, offsets, out_dtype=FP32)
+    drows = bm.beam_moe_grouped_gemm_dgrad(dgu, w_gu, offsets)
+    dx = torch.zeros(tokens, hidden, device="cuda").index_add_(0, token, drows.float())
+
+    # the same in 64 bits by automatic differentiation, every expert over every row
+    xd, gud, dd = (t.double().requires_grad_() for t in (x, w_gu, w_d))
+    mask = torch.nn.functional.one_hot(flat[order], experts).double()
+    a = torch.einsum("rk,enk,re->rn", xd[token], gud, mask)
+    gd, ud = a.chunk(2, 1)
+    yd = torch.einsum("rk,enk,re->rn", torch.nn.functional.silu(gd) * ud, dd, mask)
+    ref = torch.zeros(tokens, hidden, dtype=torch.float64, device="cuda").index_add(0, token, yd * slot_w.double())
+    gx, ggu, gd_ = torch.autograd.grad((ref * dout.double()).sum(), (xd, gud, dd))
+    # Between the inputs and any of these results lie at most five roundings to BF16, each at most
+    # 2^-8 of the value; carried through products of random rows a relative error keeps its size.
+    for got, want in ((out, ref), (dx, gx), (dw_gu, ggu), (dw_d, gd_)):
+        assert bool(((got.double() - want).norm() <= 5 * 2.0 ** -8 * want.norm()))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("tokens", [1, 200])
+def test_projections_in_4_bits_one_after_another(bm, fmt, tokens):
+    # x -> w1 -> w2, activations quantised on the way: every stage against 64 bits on the operands
+    # that the stage read
+    x = _draw((tokens, 512), BF16, 6)
+    quantised = [bm.beam_moe_quantize_fp4(_draw(s, FP32, 7 + i, 0.05), fmt) for i, s in enumerate(((320, 512), (96, 320)))]
+    v = x
+    for w in quantised:
+        q = bm.beam_moe_quantize_fp4(v, fmt)
+        nxt = bm.beam_moe_gemm_fp4(q[0], q[1], w[0], w[1], fmt, alpha_a=q[2], alpha_b=w[2], out_dtype=BF16)
+        a, b = (bm.beam_moe_dequantize_fp4(t[0], t[1], fmt, alpha=t[2], out_dtype=FP32).double() for t in (q, w))
+        ref, k = a @ b.t(), a.shape[1]
+        # the values read back are rounded to FP32 by alpha (2^-24 each), the sum as in the product's
+        # own tests, one rounding to BF16
+        acc = ((k + 15) // 16 * 2.0 ** -22 + 2.0 ** -21) * (a.abs() @ b.abs().t())
+        assert bool(((nxt.double() - ref).abs() <= acc + 2.0 ** -8 * (ref.abs() + acc)).all())
+        v = nxt
