@@ -61,30 +61,16 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
 }
 
 // Arrivals at a barrier of either CTA (address from map_to_cta).  Plain: releases this thread's
-// accesses to its own CTA only, which is right where what it announces are finished TMEM
-// accesses.  The relaxed one announces TMA copies (their bytes order themselves).  A release at
-// cluster scope waits for the thread's outstanding accesses; taken for every stage of a ring it
-// cost ~1200 cycles per stage.
+// accesses to its own CTA only, which is right where what it announces are finished TMEM accesses
+// or shared memory behind a proxy fence, both used only by the own SM's tensor core.  The relaxed
+// one announces TMA copies (their bytes order themselves).  A release at cluster scope waits for
+// outstanding stores; taken for every stage of a ring it cost ~1200 cycles per stage.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed_at(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // Whether the phase has completed, without suspending the thread.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -98,17 +84,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded waits (kWaitLimitNs): false, with *abort_flag set, once the wait ran past the limit or
+// Bounded wait (kWaitLimitNs): false, with *abort_flag set, once the wait ran past the limit or
 // another role gave up.  The clock is first read after kQuietTries tries (each suspends the
 // thread for a while): reading %globaltimer takes about a microsecond, which on every wait that
-// did not succeed at once held a ring stage to ~800 cycles.  kCluster: for barriers that follow
-// plain stores of the other CTA.
+// did not succeed at once held a ring stage to ~800 cycles.
 constexpr uint32_t kQuietTries = 256;
-template <bool kCluster = false>
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (i % kQuietTries == 0) {
       if (*abort_flag) return false;
       const uint64_t t = globaltimer_ns();

@@ -151,6 +151,34 @@ def test_rows_of_others_stay_out(bm, bad):
         _close(dw[e], d.t() @ v, d.abs().t() @ v.abs(), c, e)
 
 
+def test_ragged_ends_are_zeroed_in_time(bm):
+    # wgrad: every second expert's rows are NaN and none ends on a multiple of 16, so that each
+    # sum's last rows are followed by NaN; many times, with other work on the GPU
+    counts = [1, 33, 15, 17, 250, 5, 300, 63, 65, 129, 7, 47] * 4
+    n, k = 1536, 520
+    x, dy = _draw((sum(counts), k), BF16, 60), _draw((sum(counts), n), BF16, 61)
+    a = 0
+    for e, c in enumerate(counts):
+        if e % 2:
+            x[a:a + c] = float("nan")
+            dy[a:a + c] = float("inf")
+        a += c
+    off = _offsets(counts)
+    first = bm.beam_moe_grouped_gemm_wgrad(dy, x, off)
+    a = 0
+    for e, c in enumerate(counts):
+        if e % 2 == 0:
+            d, v = dy[a:a + c].double(), x[a:a + c].double()
+            _close(first[e], d.t() @ v, d.abs().t() @ v.abs(), c, e)
+        a += c
+    noise, side = torch.zeros(1 << 26, device="cuda"), torch.cuda.Stream()
+    for i in range(200):
+        with torch.cuda.stream(side):
+            noise.add_(1.0)
+        again = bm.beam_moe_grouped_gemm_wgrad(dy, x, off)
+        assert torch.equal(again[::2], first[::2]), i
+
+
 def test_row_strides(bm):
     counts, n, k = [40, 3, 90], 264, 136
     rows = sum(counts)
