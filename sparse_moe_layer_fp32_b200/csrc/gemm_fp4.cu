@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   } else if (kSplit && warp >= F4_FIRST_EPI) {
     // ------------------------------------------------------------ results of a shared tile
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;
-    const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
+    const float scale = (args.alpha_a ? __ldcg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldcg(args.alpha_b) : 1.0f);
     const Fp4Tile t = fp4_tile(args, first_tile);
     const bool ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_full, 0, abort_flag));
     tc_fence_after();
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   } else if (warp >= F4_FIRST_EPI) {
     // ------------------------------------------------------------ results
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;  // 64 columns of a lane quarter
-    const float scale = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
+    const float scale = (args.alpha_a ? __ldcg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldcg(args.alpha_b) : 1.0f);
     // two features of a row go as one 4-byte store where every row starts on 4 bytes
     const bool pairs =
         ((args.n | args.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(args.out) & 3) == 0;
@@ -527,8 +527,8 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
                                              void* stream) {
   if (m < 0 || n < 0 || k < 1 || (format != BEAM_MOE_FP4_MX && format != BEAM_MOE_FP4_NV)) return BEAM_MOE_ERR_INVALID_ARG;
   if (out_type != BEAM_MOE_BF16 && out_type != BEAM_MOE_FP16 && out_type != BEAM_MOE_FP32) return BEAM_MOE_ERR_INVALID_ARG;
-  if (k % 32 != 0 || m > 0x7fff0000 || n > 0x7fff0000) return BEAM_MOE_ERR_UNSUPPORTED;
-  if ((static_cast<int64_t>(m) + 255) / 256 * ((static_cast<int64_t>(n) + 255) / 256) > INT32_MAX / 2)
+  if (k % 32 != 0 || m > 0x7fff0000 || n > 0x7fff0000 || k > 0x7fff0000) return BEAM_MOE_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(m) + 255) / 256 * ((static_cast<int64_t>(n) + 255) / 256) > (1 << 30))
     return BEAM_MOE_ERR_UNSUPPORTED;
   if (m == 0 || n == 0) return BEAM_MOE_OK;
   const int64_t scales = k / (format == BEAM_MOE_FP4_MX ? 32 : 16);
@@ -547,7 +547,7 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
       !make_bytes_map(&maps.n_codes, a_codes, k / 2, m, lda, 128, height / 2, true) ||
       !make_bytes_map(&maps.m_sf, b_sf, scales, n, ldb_sf, 16, 128, false) ||
       !make_bytes_map(&maps.n_sf, a_sf, scales, m, lda_sf, 16, height, false))
-    return BEAM_MOE_ERR_INVALID_ARG;
+    return BEAM_MOE_ERR_UNSUPPORTED;  // strides that a tensor map cannot hold
   // MXFP4 has no tensor scale
   const Fp4Args args{m, n, k, blocks, height, 1, mx ? nullptr : alpha_a, mx ? nullptr : alpha_b, out, ldo};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -178,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
   pdl_trigger();
   // The groups' borders and first tiles.
   for (int e = threadIdx.x; e <= args.groups; e += GG_THREADS)
-    tail->begin[e] = min(max(__ldg(args.offsets + e), 0), args.rows);
+    tail->begin[e] = min(max(__ldcg(args.offsets + e), 0), args.rows);
   __syncthreads();
   if (warp == 0) {
     const int mt = (args.m + GG_TILE - 1) / GG_TILE;
@@ -377,11 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
     const int side = w >> 2;               // and its half of the columns
     int acc = 0;
     uint32_t acc_phase = 0;
+    // Once a wait gave up, the tiles are gone through without waits and without stores to the end:
+    // the warps that share a named barrier meet at it all the same.
+    bool ok = true;
     for (int id = first_tile; id < total; id += tile_stride) {
       const GroupedTile t = grouped_tile<MODE>(args, tail, id);
       const bool any = t.steps > 0;
       if (any) {
-        if (!__all_sync(0xffffffffu, pair_wait(&tail->acc_full[acc], acc_phase, abort_flag))) break;
+        ok = ok && __all_sync(0xffffffffu, pair_wait(&tail->acc_full[acc], acc_phase, abort_flag));
         tc_fence_after();
       }
       const int m = t.m0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
@@ -427,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             for (int i = 0; i < 4; ++i) {
               const int r = 8 * i + sub, row = m - lane + r;
               const uint4 q = *reinterpret_cast<const uint4*>(tile + r * 64 + ((part ^ ((r >> 1) & 3)) << 4));
-              if (row < args.m && col < args.ncols)
+              if (ok && row < args.m && col < args.ncols)
                 *reinterpret_cast<uint4*>(static_cast<uint8_t*>(args.out) +
                                           ((static_cast<int64_t>(t.group) * args.m + row) * args.ncols + col) * kBytes) = q;
             }
@@ -439,10 +442,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             float* p = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo + m;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (row + j < t.n_end && m < args.m) p[j * args.ldo] = __uint_as_float(v[j]);
+              if (ok && row + j < t.n_end && m < args.m) p[j * args.ldo] = __uint_as_float(v[j]);
           } else {
             store_turned<OUT>(v, 1.0f, tail->turn + side * 8192, 1 + side, quarter, lane,
-                              static_cast<uint16_t*>(args.out), args.ldo, row, t.n_end,
+                              static_cast<uint16_t*>(args.out), args.ldo, row, ok ? t.n_end : row,
                               t.m0 + static_cast<int>(rank) * 128, args.m);
           }
         }
@@ -530,7 +533,7 @@ cudaError_t launch_grouped_gemm(int mode, const void* rows_a, int64_t ld_a, cons
          make_map(&mb, bf16, rows_a, 2, mode == kFwd ? k : n, rows, 1, ld_a * 2, 0, 64, GG_BOX_ROWS) &&
          make_map(&mb2, bf16, rows_a, 2, mode == kFwd ? k : n, rows, 1, ld_a * 2, 0, 64, 128);
   }
-  if (!ok) return cudaErrorInvalidValue;
+  if (!ok) return cudaErrorNotSupported;  // strides that a tensor map cannot hold
   const int64_t tiles = grouped_gemm_most_tiles(mode, rows, groups, n, k);
   if (mode == kFwd) return launch_out<kFwd>(out_type, a, ma, mb, mb2, tiles, s);
   if (mode == kDgrad) return launch_out<kDgrad>(out_type, a, ma, mb, mb2, tiles, s);
@@ -554,14 +557,18 @@ beam_moe_status check_grouped(int32_t rows, int32_t groups, int32_t n, int32_t k
   if (rows < 0 || groups < 1 || n < 1 || k < 1) return BEAM_MOE_ERR_INVALID_ARG;
   if ((type != BEAM_MOE_BF16 && type != BEAM_MOE_FP16) || (out_type != type && out_type != BEAM_MOE_FP32))
     return BEAM_MOE_ERR_INVALID_ARG;
-  if (n % 8 != 0 || k % 8 != 0 || groups > GG_MAX_GROUPS || rows > 0x7fff0000) return BEAM_MOE_ERR_UNSUPPORTED;
+  // 2^30: features and tile numbers stay in 32 bits with a tile or a grid to spare
+  if (n % 8 != 0 || k % 8 != 0 || n > (1 << 30) || k > (1 << 30) || groups > GG_MAX_GROUPS || rows > 0x7fff0000)
+    return BEAM_MOE_ERR_UNSUPPORTED;
   return BEAM_MOE_OK;
 }
 
 // A [rows][cols] operand whose rows are ld elements apart.
 bool good_rows(const void* p, int64_t ld, int32_t cols) { return p && aligned16(p) && ld >= cols && ld % 8 == 0; }
 
-beam_moe_status launch_status(cudaError_t e) { return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA; }
+beam_moe_status launch_status(cudaError_t e) {
+  return e == cudaSuccess ? BEAM_MOE_OK : e == cudaErrorNotSupported ? BEAM_MOE_ERR_UNSUPPORTED : BEAM_MOE_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -572,7 +579,7 @@ beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w,
                                       int32_t out_type, void* stream) {
   const beam_moe_status st = check_grouped(rows, groups, n, k, type, out_type);
   if (st != BEAM_MOE_OK) return st;
-  if (grouped_gemm_most_tiles(kFwd, rows, groups, n, k) > INT32_MAX) return BEAM_MOE_ERR_UNSUPPORTED;
+  if (grouped_gemm_most_tiles(kFwd, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
   if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
@@ -586,7 +593,7 @@ beam_moe_status beam_moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const 
                                             int64_t lddx, int32_t out_type, void* stream) {
   const beam_moe_status st = check_grouped(rows, groups, n, k, type, out_type);
   if (st != BEAM_MOE_OK) return st;
-  if (grouped_gemm_most_tiles(kDgrad, rows, groups, n, k) > INT32_MAX) return BEAM_MOE_ERR_UNSUPPORTED;
+  if (grouped_gemm_most_tiles(kDgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
   if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
@@ -600,7 +607,7 @@ beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const 
                                             int32_t type, void* dw, int32_t out_type, void* stream) {
   const beam_moe_status st = check_grouped(rows, groups, n, k, type, out_type);
   if (st != BEAM_MOE_OK) return st;
-  if (grouped_gemm_most_tiles(kWgrad, rows, groups, n, k) > INT32_MAX) return BEAM_MOE_ERR_UNSUPPORTED;
+  if (grouped_gemm_most_tiles(kWgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (!dw || !aligned16(dw)) return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0)  // no rows: every gradient is zero

@@ -33,11 +33,11 @@ constexpr int kPieceValues = 256;
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
   if constexpr (TYPE == kTypeFp32) {
-    const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
+    const float4 a = __ldcg(static_cast<const float4*>(p)), b = __ldcg(static_cast<const float4*>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
-    const uint4 q = __ldg(static_cast<const uint4*>(p));
+    const uint4 q = __ldcg(static_cast<const uint4*>(p));
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -53,11 +53,13 @@ __device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
   }
 }
 
-// One 32-byte load of memory that the kernel does not write, from a 32-byte boundary.
+// One 32-byte load from a 32-byte boundary.  (Not through the read-only path, here and below: the
+// kernel may have started before the one that writes the memory ended.)
 __device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* w) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
+               : "l"(p)
+               : "memory");
 }
 
 // A block as it lies in memory, in 32-bit words (two 16-bit values or one FP32 value each).
@@ -75,7 +77,7 @@ struct RawBlock {
     }
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 q = __ldg(static_cast<const uint4*>(p) + i);
+      const uint4 q = __ldcg(static_cast<const uint4*>(p) + i);
       w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
     }
   }
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
   const uint32_t threads = gridDim.x * 256u;
   float alpha = 0.0f, six_alpha = 0.0f;
   if (!kMx) {
-    alpha = amax_dev ? __fdiv_rn(*amax_dev, 2688.0f) : alpha_param;
+    alpha = amax_dev ? __fdiv_rn(__ldcg(amax_dev), 2688.0f) : alpha_param;
     six_alpha = __fmul_rn(6.0f, alpha);
     if (alpha_out && blockIdx.x == 0 && threadIdx.x == 0) *alpha_out = alpha;
   }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
   pdl_wait();
   pdl_trigger();
   const uint32_t threads = gridDim.x * 256u;
-  const float alpha = !kMx && alpha_dev ? *alpha_dev : 1.0f;
+  const float alpha = !kMx && alpha_dev ? __ldcg(alpha_dev) : 1.0f;
   for (uint32_t q0 = blockIdx.x * 256u + threadIdx.x; q0 < pieces.total; q0 += threads * kAtOnce) {
     uint32_t word[kAtOnce][V / 8], scale[kAtOnce], row[kAtOnce], part[kAtOnce];
 #pragma unroll
@@ -293,13 +295,13 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
       if (q < pieces.total) {
         const uint8_t* c = codes + row[u] * ldc + static_cast<int64_t>(part[u]) * (V / 2);
         if constexpr (V == 16) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(c));
+          const uint2 w = __ldcg(reinterpret_cast<const uint2*>(c));
           word[u][0] = w.x;
           word[u][1] = w.y;
         } else {
-          word[u][0] = __ldg(reinterpret_cast<const uint32_t*>(c));
+          word[u][0] = __ldcg(reinterpret_cast<const uint32_t*>(c));
         }
-        scale[u] = __ldg(sf + row[u] * ldsf + static_cast<int64_t>(part[u]) * V / (kMx ? 32 : 16));
+        scale[u] = __ldcg(sf + row[u] * ldsf + static_cast<int64_t>(part[u]) * V / (kMx ? 32 : 16));
       }
     }
 #pragma unroll

@@ -6,6 +6,10 @@ sum is aligned to its largest term and cut off below FP32's last bit (the next p
 bounds its growth), at most 2^-22 of S = sum |a||b| for each 16 terms; NVFP4's two tensor scales
 multiply once each, 2^-24 of the value twice; then one rounding to the output's type."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -249,6 +253,37 @@ def test_the_library_quantisers_weights(bm):
     y = bm.beam_moe_gemm_fp4(qx[0], qx[1], qw[0], qw[1], "nvfp4", alpha_a=qx[2], alpha_b=qw[2], out_dtype=FP32)
     va, vb = _values(qx[0], qx[1], "nvfp4", qx[2].item()), _values(qw[0], qw[1], "nvfp4", qw[2].item())
     _close(y, va @ vb.t(), va.abs() @ vb.abs().t(), 512)
+
+
+def test_single_rows_of_any_pitch(bm):
+    # the distance to a row that is not there does not matter
+    for fmt in ("mxfp4", "nvfp4"):
+        x = _draw((1, 67 + 64), BF16, 40)[:, :64]
+        q = bm.beam_moe_quantize_fp4(x, fmt)
+        assert all(torch.equal(a, b) for a, b in zip(q[:2], bm.beam_moe_quantize_fp4(x.contiguous(), fmt)[:2]))
+        w = bm.beam_moe_quantize_fp4(_draw((24, 64), BF16, 41), fmt)
+        y = bm.beam_moe_gemm_fp4(q[0], q[1].contiguous(), w[0], w[1], fmt, alpha_a=q[2], alpha_b=w[2])
+        assert torch.equal(y, bm.beam_moe_gemm_fp4(q[0], q[1], w[0], w[1], fmt, alpha_a=q[2], alpha_b=w[2]))
+
+
+def test_captured_before_any_other_call():
+    # the first use of the kernels in a process may be inside a capture
+    code = (
+        "import torch, sparse_moe_layer_fp32_b200 as bm\n"
+        "x = torch.randn(40, 256, device='cuda').bfloat16(); w = torch.randn(3, 64, 256, device='cuda').bfloat16()\n"
+        "off = torch.tensor([0, 10, 10, 40], dtype=torch.int32, device='cuda')\n"
+        "torch.cuda.synchronize(); g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    y = bm.beam_moe_grouped_gemm(x, w, off); dw = bm.beam_moe_grouped_gemm_wgrad(y, x, off)\n"
+        "    q = bm.beam_moe_quantize_fp4(x, 'nvfp4'); z = bm.beam_moe_gemm_fp4(q[0], q[1], q[0], q[1], 'nvfp4')\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "assert torch.equal(y, bm.beam_moe_grouped_gemm(x, w, off)), 'forward'\n"
+        "assert torch.equal(dw, bm.beam_moe_grouped_gemm_wgrad(y, x, off)), 'wgrad'\n"
+        "assert torch.equal(z, bm.beam_moe_gemm_fp4(q[0], q[1], q[0], q[1], 'nvfp4')), 'product'\n"
+        "bm.beam_moe_check_operators(); print('fine')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "fine" in done.stdout, done.stderr[-2000:]
 
 
 def test_nothing_to_do(bm):

@@ -53,6 +53,8 @@ def test_grouped_products(name):
         assert _grouped(name, rows=0, a=None, c=None) == OK  # nothing to do
         # more output tiles than the kernel numbers
         assert _grouped(name, rows=2**31 - 2**17, n=2**30, k=2**30) == UNSUPPORTED
+        assert _grouped(name, n=2**30 + 8) == UNSUPPORTED
+        assert _grouped(name, k=2**30 + 8) == UNSUPPORTED
 
 
 def _quantize(form=0, src=P, t=bm.TYPE_BF16, ld=64, rows=4, cols=64, alpha=1.0, codes=P, ldc=32, sf=P, ldsf=16,
@@ -108,6 +110,7 @@ def test_fp4_product():
         assert _gemm(form=form, k=0) == BAD
         assert _gemm(form=form, k=48) == UNSUPPORTED
         assert _gemm(form=form, m=2**31 - 1) == UNSUPPORTED
+        assert _gemm(form=form, k=2**31 - 32) == UNSUPPORTED
         assert _gemm(form=form, m=2**30, n=2**30, ldo=2**30) == UNSUPPORTED
         assert _gemm(form=form, t=5) == BAD
         assert _gemm(form=form, m=0) == OK
