@@ -394,17 +394,17 @@ def _grouped(offsets, a, b):
     return kind
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory that belongs to the stream which writes it."""
+def _empty(like, shape, dtype, stream):
+    """Memory on like's device that belongs to the stream which writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _output(out, shape, dtype, device, stream):
+def _output(out, like, shape, dtype, stream):
     if out is None:
-        return _empty(shape, dtype, device, stream)
+        return _empty(like, shape, dtype, stream)
     if out.shape != shape or out.dtype not in TYPES:
         raise ValueError(f"out has to be a BF16, FP16 or FP32 tensor of shape {shape}")
     return out
@@ -428,7 +428,7 @@ def beam_moe_grouped_gemm(x, w, offsets, out=None, out_dtype=None, stream=None):
     rows = x.shape[0]
     if x.shape[1] != k:
         raise ValueError(f"x has {x.shape[1]} columns and w {k}")
-    y = _output(out, (rows, n), out_dtype or kind, x.device, stream)
+    y = _output(out, x, (rows, n), out_dtype or kind, stream)
     _call("beam_moe_grouped_gemm", _device_index(x, w, offsets, y), stream, x.data_ptr(), ldx, w.data_ptr(),
           offsets.data_ptr(), rows, groups, n, k, TYPES[kind], y.data_ptr(), _row_stride(y, "out"), TYPES[y.dtype])
     return y
@@ -445,7 +445,7 @@ def beam_moe_grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream
     rows = dy.shape[0]
     if dy.shape[1] != n:
         raise ValueError(f"dy has {dy.shape[1]} columns and w {n} rows")
-    dx = _output(out, (rows, k), out_dtype or kind, dy.device, stream)
+    dx = _output(out, dy, (rows, k), out_dtype or kind, stream)
     _call("beam_moe_grouped_gemm_dgrad", _device_index(dy, w, offsets, dx), stream, dy.data_ptr(), lddy, w.data_ptr(),
           offsets.data_ptr(), rows, groups, n, k, TYPES[kind], dx.data_ptr(), _row_stride(dx, "out"), TYPES[dx.dtype])
     return dx
@@ -462,7 +462,7 @@ def beam_moe_grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, stream
     groups, k = offsets.shape[0] - 1, x.shape[1]
     if x.shape[0] != rows:
         raise ValueError(f"dy has {rows} rows and x {x.shape[0]}")
-    dw = _output(out, (groups, n, k), out_dtype or kind, dy.device, stream)
+    dw = _output(out, dy, (groups, n, k), out_dtype or kind, stream)
     if not dw.is_contiguous():
         raise ValueError("out has to be contiguous")
     _call("beam_moe_grouped_gemm_wgrad", _device_index(dy, x, offsets, dw), stream, dy.data_ptr(), lddy, x.data_ptr(),
@@ -516,12 +516,12 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     rows, cols = src.shape
     blocks = cols // FP4_BLOCK[fmt]
     pitch = (blocks + 15) // 16 * 16
-    index, device = _device_index(src), src.device
-    codes = _empty((rows, cols // 2), torch.uint8, device, stream)
-    sf = _empty((rows, pitch), torch.uint8, device, stream)
+    index = _device_index(src)
+    codes = _empty(src, (rows, cols // 2), torch.uint8, stream)
+    sf = _empty(src, (rows, pitch), torch.uint8, stream)
     scale = None
     if fmt == "nvfp4":  # the library writes it; an empty tensor has none
-        scale = _empty((1,), torch.float32, device, stream) if rows and cols else torch.zeros(1, device=device)
+        scale = _empty(src, (1,), torch.float32, stream) if rows and cols else src.new_zeros(1, dtype=torch.float32)
     _call("beam_moe_quantize_fp4", index, stream, form, src.data_ptr(), kind, ld, rows, cols,
           -1.0 if alpha is None else alpha, codes.data_ptr(), cols // 2, sf.data_ptr(), pitch,
           None if scale is None else scale.data_ptr())
@@ -536,7 +536,7 @@ def beam_moe_dequantize_fp4(codes, sf, fmt, alpha=None, out_dtype=torch.bfloat16
     if out_dtype not in TYPES:
         raise ValueError("out_dtype has to be BF16, FP16 or FP32")
     index = _device_index(codes, sf, alpha)
-    out = _empty((rows, cols), out_dtype, codes.device, stream)
+    out = _empty(codes, (rows, cols), out_dtype, stream)
     _call("beam_moe_dequantize_fp4", index, stream, form, codes.data_ptr(), ldc, sf.data_ptr(), ldsf,
           None if alpha is None else alpha.data_ptr(), rows, cols, out.data_ptr(), TYPES[out_dtype], cols)
     return out
@@ -553,7 +553,7 @@ def beam_moe_gemm_fp4(a_codes, a_sf, b_codes, b_sf, fmt, alpha_a=None, alpha_b=N
     if k != kb:
         raise ValueError(f"a has {k} columns and b {kb}")
     alpha_a, alpha_b = _tensor_scale(alpha_a, fmt, "alpha_a"), _tensor_scale(alpha_b, fmt, "alpha_b")
-    out = _output(out, (m, n), out_dtype or torch.bfloat16, a_codes.device, stream)
+    out = _output(out, a_codes, (m, n), out_dtype or torch.bfloat16, stream)
     _call("beam_moe_gemm_fp4", _device_index(a_codes, a_sf, b_codes, b_sf, alpha_a, alpha_b, out), stream, form,
           a_codes.data_ptr(), lda, a_sf.data_ptr(), lda_sf, None if alpha_a is None else alpha_a.data_ptr(),
           b_codes.data_ptr(), ldb, b_sf.data_ptr(), ldb_sf, None if alpha_b is None else alpha_b.data_ptr(), m, n, k,
