@@ -31,6 +31,13 @@
 // Tiles are dealt out round robin; the order keeps the tiles that run together on the same
 // weights (forward, dgrad) or the same expert (wgrad), whose operands L2 then holds.
 //
+// What bounds it.  A stage of an n-row tile is 2 n cycles of MMAs against about 256 + n for its
+// operands on their way through L2 and shared memory: they meet at 256 rows, where the tensor pipe
+// is active 89% of the cycles and the power limit sets the clock (16384 x 5120 x 5120 BF16 in
+// one group: 556 us, 1540 TFLOP/s, cuBLAS 550; 32 experts of 512 rows each, 5120 x 5120: 626 us).
+// Uneven experts lose to tiles of fewer rows (702 us).  With a row or a few for each expert it
+// streams weights: 64 rows over 256 experts of 1536 x 5120 in 151 us, 5.9 TB/s.
+//
 // The work list comes from the offsets, which only the device knows: every CTA scans them at
 // its start (at most 1024 experts).  They are read as their running maximum, clamped to
 // [0, rows], so no offsets can make the kernel leave its buffers.
