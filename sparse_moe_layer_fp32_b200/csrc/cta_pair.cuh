@@ -202,10 +202,19 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   }
 }
 
+// Lanes hold feature `lane` of two rows (lo, hi as FP32 bits); each gets two features of one row: an
+// even lane its own and the next lane's of the first row, an odd one the lane before's and its
+// own of the second.
+template <int OUT>
+__device__ __forceinline__ uint32_t trade_pair(uint32_t lo, uint32_t hi, float scale, int odd) {
+  const uint32_t mine = pack_pair<OUT>(__uint_as_float(lo) * scale, __uint_as_float(hi) * scale);
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  return __byte_perm(mine, other, odd ? 0x3276u : 0x5410u);
+}
+
 // Accumulators whose lanes are features and whose columns are rows of the output, stored in rows:
 // four warps (one per lane quarter) hold 32 columns of this CTA's 128 features; v: this lane's
-// feature in rows row0 .. row0 + 31.  Neighbouring lanes trade values so that each has two
-// features of one row; the 32 x 128 values are turned in 8 KB of shared memory and leave as whole
+// feature in rows row0 .. row0 + 31.  The 32 x 128 values are turned in 8 KB of shared memory and leave as whole
 // 256-byte rows (against 64-byte pieces straight from the lanes: 1% less time for the grouped
 // products; the 4-bit product, which shared memory bounds, is 2 to 4% faster without).  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
 // barrier: a named barrier of these four warps.
@@ -218,9 +227,7 @@ __device__ __forceinline__ void store_turned(const uint32_t (&v)[32], float scal
   uint8_t* to = turn + odd * 256 + ((quarter * 64 + (lane - odd) * 2) ^ (odd << 6));
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const float mine = __uint_as_float(odd ? v[j + 1] : v[j]) * scale;
-    const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1)) * scale;
-    *reinterpret_cast<uint32_t*>(to + j * 256) = odd ? pack_pair<OUT>(other, mine) : pack_pair<OUT>(mine, other);
+    *reinterpret_cast<uint32_t*>(to + j * 256) = trade_pair<OUT>(v[j], v[j + 1], scale, odd);
   }
   asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
   const int part = lane & 15, f = f0 + part * 8;
