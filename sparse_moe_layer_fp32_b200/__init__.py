@@ -352,14 +352,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _device_index(first, *others):
     """Number of the CUDA device that holds all the tensors (None stands for one not given)."""
-    device = first.device
-    same = device.type == "cuda"
+    index = first.get_device()  # -1 on the CPU
+    same = first.is_cuda
     for t in others:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             same = False
     if not same:
         raise ValueError("the tensors have to be on one CUDA device")
-    return device.index
+    return index
 
 
 def _call(name, index, stream, *args):
@@ -479,15 +479,16 @@ def _fp4_format(fmt):
 
 def _fp4_matrix(codes, sf, fmt, what):
     """(rows, cols, bytes between rows of codes, of scales) of a quantised matrix."""
-    if codes.dtype is not torch.uint8 or sf.dtype is not torch.uint8:
-        raise ValueError(f"{what}'s codes and scales have to be uint8 tensors")
-    ldc, ldsf = _row_stride(codes, what), _row_stride(sf, what)
-    rows, half = codes.shape
-    blocks = 2 * half // FP4_BLOCK[fmt]
-    if sf.shape != (rows, blocks):
+    if codes.dtype is not torch.uint8 or sf.dtype is not torch.uint8 or codes.dim() != 2 or sf.dim() != 2:
+        raise ValueError(f"{what}'s codes and scales have to be 2-D uint8 tensors")
+    (rows, half), (sf_rows, blocks) = codes.shape, sf.shape
+    if sf_rows != rows or blocks != 2 * half // FP4_BLOCK[fmt]:
         raise ValueError(f"{what} has to be codes [rows, cols / 2] and scales [rows, cols / {FP4_BLOCK[fmt]}]")
-    if rows <= 1:  # never stepped over: any pitch that the library takes will do
-        ldsf = (ldsf + 15) // 16 * 16
+    (ldc, inner), (ldsf, sf_inner) = codes.stride(), sf.stride()
+    if (inner != 1 and half > 1) or (sf_inner != 1 and blocks > 1):
+        raise ValueError(f"the columns of {what}'s codes and scales have to lie next to one another")
+    if rows <= 1:  # a single row's pitch is never stepped over: any that the library takes will do
+        ldc, ldsf = half, (blocks + 15) // 16 * 16
     return rows, 2 * half, ldc, ldsf
 
 

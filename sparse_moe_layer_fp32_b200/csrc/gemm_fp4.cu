@@ -325,24 +325,27 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
           }
           tmem_st_32x32b_x16(col + F4_SF_N, w);
         } else {
+          // all loads first: the stores of one part would hold up the next part's loads
+          uint4 v[12];
+#pragma unroll
+          for (int q = 0; q < 12; ++q)
+            v[q] = *reinterpret_cast<const uint4*>(q < 4 ? sm + q * 512 : sn + (q - 4) * 512);
           uint32_t r[16];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sm + q * 512);
-            r[q] = v.x;
-            r[4 + q] = v.y;
-            r[8 + q] = v.z;
-            r[12 + q] = v.w;
+            r[q] = v[q].x;
+            r[4 + q] = v[q].y;
+            r[8 + q] = v[q].z;
+            r[12 + q] = v[q].w;
           }
           tmem_st_32x32b_x16(col, r);
           uint32_t w[32];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sn + q * 512);
-            w[q] = v.x;
-            w[8 + q] = v.y;
-            w[16 + q] = v.z;
-            w[24 + q] = v.w;
+            w[q] = v[4 + q].x;
+            w[8 + q] = v[4 + q].y;
+            w[16 + q] = v[4 + q].z;
+            w[24 + q] = v[4 + q].w;
           }
           tmem_st_32x32b_x32(col + F4_SF_N, w);
         }
