@@ -216,7 +216,7 @@ __device__ __forceinline__ uint32_t trade_pair(uint32_t lo, uint32_t hi, float s
 // four warps (one per lane quarter) hold 32 columns of this CTA's 128 features; v: this lane's
 // feature in rows row0 .. row0 + 31.  The 32 x 128 values are turned in 8 KB of shared memory and leave as whole
 // 256-byte rows (against 64-byte pieces straight from the lanes: 1% less time for the grouped
-// products; the 4-bit product, which shared memory bounds, is 2 to 4% faster without).  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
+// products; the 4-bit product is 3 to 9% faster without).  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
 // barrier: a named barrier of these four warps.
 template <int OUT>
 __device__ __forceinline__ void store_turned(const uint32_t (&v)[32], float scale, uint8_t* turn, int barrier, int quarter,

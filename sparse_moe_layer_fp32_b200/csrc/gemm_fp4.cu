@@ -28,11 +28,12 @@
 // columns (the scales of five stages take the other half of TMEM): the storing warps read it
 // into registers and release it before they convert and store.
 //
-// What bounds it.  16384 x 5120 x 5120: MXFP4 178 us (4.8 PFLOP/s), NVFP4 190; the tensor pipe is
-// active 57% of the cycles, the MMAs wait for the accumulator's drain between tiles (30%) and for
-// scales; in a long loop the power limit sets the clock (1.5 GHz, 204 and 217 us).  Two sets of
-// scale warps, results turned in shared memory, sleeping waits: none was faster.  One token, 5120 x
-// 5120: 6.0 us with the weights in L2, 7.6 without, of which a launch with one K step is 3.7.
+// What bounds it.  16384 x 5120 x 5120: MXFP4 174 us (4.9 PFLOP/s), NVFP4 187; the tensor pipe is
+// active 60% of the cycles, the MMAs wait for the accumulator's drain between tiles and for
+// stages (a ring of four: 8% slower); in a long loop the power limit sets the clock (1.5 GHz, 202 and
+// 217 us).  A second set of scale warps, results turned in shared memory, sleeping waits: each was
+// slower.  One token, 5120 x 5120: 6.0 us with the weights in L2, 7.6 without, of which a launch
+// with one K step is 3.7.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
