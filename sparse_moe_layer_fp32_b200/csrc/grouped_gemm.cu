@@ -588,7 +588,7 @@ beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w,
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kFwd, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || !offsets ||
+  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || y == x || y == w || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kFwd, x, ldx, nullptr, 0, w, offsets, rows, groups, n, k, type, y, ldy,
@@ -602,7 +602,7 @@ beam_moe_status beam_moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const 
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kDgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || !offsets ||
+  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || dx == dy || dx == w || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kDgrad, dy, lddy, nullptr, 0, w, offsets, rows, groups, n, k, type, dx,
@@ -620,7 +620,8 @@ beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const 
   if (rows == 0)  // no rows: every gradient is zero
     return launch_status(cudaMemsetAsync(
         dw, 0, static_cast<size_t>(groups) * n * static_cast<size_t>(k) * (out_type == BEAM_MOE_FP32 ? 4 : 2), s));
-  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 3))
+  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || dw == dy || dw == x || !offsets ||
+      (reinterpret_cast<uintptr_t>(offsets) & 3))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kWgrad, x, ldx, dy, lddy, nullptr, offsets, rows, groups, n, k, type, dw, k,
                                            out_type, s));

@@ -109,8 +109,8 @@ struct RawBlock {
 
 // A matrix cut into pieces, per_row to a row: blocks of 16 or 32 values, or 256 values of a row,
 // the last such piece of a row shorter.  A matrix whose rows lie end to end in every array is one
-// long row.  Rows are split from piece numbers by
-// a multiplication: magic = min(2^32 - 1, floor(2^32 / per_row)) is too small by less than one.
+// long row.  Rows are split from piece numbers by a multiplication; with magic =
+// min(2^32 - 1, floor(2^32 / per_row)) the quotient is right or one too small.
 struct Pieces {
   uint32_t total, per_row, magic;
 };
@@ -420,7 +420,8 @@ cudaError_t launch_dequantize(int out_type, const uint8_t* codes, int64_t ldc, c
 beam_moe_status check_fp4(int32_t format, int64_t rows, int32_t cols, int32_t type) {
   if (rows < 0 || cols < 0 || (format != BEAM_MOE_FP4_MX && format != BEAM_MOE_FP4_NV)) return BEAM_MOE_ERR_INVALID_ARG;
   if (type != BEAM_MOE_BF16 && type != BEAM_MOE_FP16 && type != BEAM_MOE_FP32) return BEAM_MOE_ERR_INVALID_ARG;
-  if (cols % 32 != 0 || rows > (int64_t{1} << 40)) return BEAM_MOE_ERR_UNSUPPORTED;
+  // 2^46 values: products of rows and columns stay far inside 64 bits
+  if (cols % 32 != 0 || rows > (int64_t{1} << 46) / std::max(cols, 32)) return BEAM_MOE_ERR_UNSUPPORTED;
   return BEAM_MOE_OK;
 }
 int scale_bytes(int32_t format, int32_t cols) { return cols / (format == BEAM_MOE_FP4_MX ? 32 : 16); }

@@ -9,7 +9,7 @@ BAD, UNSUPPORTED, OK = bm.ERR_INVALID_ARG, bm.ERR_UNSUPPORTED, bm.OK
 P = 1 << 20  # an aligned address that nothing reads: every call below is refused
 
 
-def _grouped(name, rows=4, groups=2, n=16, k=32, t=bm.TYPE_BF16, out_type=bm.TYPE_BF16, a=P, b=P, c=P, off=P,
+def _grouped(name, rows=4, groups=2, n=16, k=32, t=bm.TYPE_BF16, out_type=bm.TYPE_BF16, a=P, b=P, c=2 * P, off=P,
              lda=None, ldb=None, ldc=None):
     lib = bm.lib()
     if name == "beam_moe_grouped_gemm_wgrad":
@@ -38,9 +38,11 @@ def test_grouped_products(name):
     assert _grouped(name, b=None) == BAD
     assert _grouped(name, c=None) == BAD
     assert _grouped(name, off=None) == BAD
+    assert _grouped(name, a=P, b=3 * P, c=P) == BAD         # the output is an operand
+    assert _grouped(name, a=3 * P, b=P, c=P) == BAD
     assert _grouped(name, a=P + 8) == BAD
     assert _grouped(name, b=P + 2) == BAD
-    assert _grouped(name, c=P + 4) == BAD
+    assert _grouped(name, c=2 * P + 4) == BAD
     assert _grouped(name, off=P + 2) == BAD
     assert _grouped(name, lda=8) == BAD                     # shorter than a row
     assert _grouped(name, lda=36) == BAD                    # rows off 16-byte boundaries
@@ -80,6 +82,7 @@ def test_fp4_quantiser():
             assert call(form=2) == BAD
             assert call(form=form, t=3) == BAD
             assert call(form=form, cols=48) == UNSUPPORTED
+            assert call(form=form, rows=2**60) == UNSUPPORTED
             assert call(form=form, rows=0) == OK
             assert call(form=form, cols=0) == OK
             assert call(form=form, codes=None) == BAD
