@@ -374,6 +374,13 @@ def _call(name, index, stream, *args):
         raise BeamMoeError(status, name)
 
 
+def _fits_int32(name, *sizes):
+    """The C arguments are 32 bits wide, and ctypes would cut larger sizes off without a word."""
+    for size in sizes:
+        if size > 0x7FFFFFFF:
+            raise BeamMoeError(ERR_UNSUPPORTED, name)
+
+
 def _row_stride(t, what):
     """Elements from one row of a 2-D tensor to the next."""
     if t.dim() != 2:
@@ -428,6 +435,7 @@ def beam_moe_grouped_gemm(x, w, offsets, out=None, out_dtype=None, stream=None):
     rows = x.shape[0]
     if x.shape[1] != k:
         raise ValueError(f"x has {x.shape[1]} columns and w {k}")
+    _fits_int32("beam_moe_grouped_gemm", rows, n, k)
     y = _output(out, x, (rows, n), out_dtype or kind, stream)
     _call("beam_moe_grouped_gemm", _device_index(x, w, offsets, y), stream, x.data_ptr(), ldx, w.data_ptr(),
           offsets.data_ptr(), rows, groups, n, k, TYPES[kind], y.data_ptr(), _row_stride(y, "out"), TYPES[y.dtype])
@@ -445,6 +453,7 @@ def beam_moe_grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream
     rows = dy.shape[0]
     if dy.shape[1] != n:
         raise ValueError(f"dy has {dy.shape[1]} columns and w {n} rows")
+    _fits_int32("beam_moe_grouped_gemm_dgrad", rows, n, k)
     dx = _output(out, dy, (rows, k), out_dtype or kind, stream)
     _call("beam_moe_grouped_gemm_dgrad", _device_index(dy, w, offsets, dx), stream, dy.data_ptr(), lddy, w.data_ptr(),
           offsets.data_ptr(), rows, groups, n, k, TYPES[kind], dx.data_ptr(), _row_stride(dx, "out"), TYPES[dx.dtype])
@@ -462,6 +471,7 @@ def beam_moe_grouped_gemm_wgrad(dy, x, offsets, out=None, out_dtype=None, stream
     groups, k = offsets.shape[0] - 1, x.shape[1]
     if x.shape[0] != rows:
         raise ValueError(f"dy has {rows} rows and x {x.shape[0]}")
+    _fits_int32("beam_moe_grouped_gemm_wgrad", rows, groups, n, k)
     dw = _output(out, dy, (groups, n, k), out_dtype or kind, stream)
     if not dw.is_contiguous():
         raise ValueError("out has to be contiguous")
@@ -515,6 +525,7 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
         raise ValueError("alpha has to be a positive finite number")
     ld = _row_stride(src, "src")
     rows, cols = src.shape
+    _fits_int32("beam_moe_quantize_fp4", cols)
     blocks = cols // FP4_BLOCK[fmt]
     pitch = (blocks + 15) // 16 * 16
     index = _device_index(src)
@@ -536,6 +547,7 @@ def beam_moe_dequantize_fp4(codes, sf, fmt, alpha=None, out_dtype=torch.bfloat16
     alpha = _tensor_scale(alpha, fmt, "alpha")
     if out_dtype not in TYPES:
         raise ValueError("out_dtype has to be BF16, FP16 or FP32")
+    _fits_int32("beam_moe_dequantize_fp4", cols)
     index = _device_index(codes, sf, alpha)
     out = _empty(codes, (rows, cols), out_dtype, stream)
     _call("beam_moe_dequantize_fp4", index, stream, form, codes.data_ptr(), ldc, sf.data_ptr(), ldsf,
@@ -554,6 +566,7 @@ def beam_moe_gemm_fp4(a_codes, a_sf, b_codes, b_sf, fmt, alpha_a=None, alpha_b=N
     if k != kb:
         raise ValueError(f"a has {k} columns and b {kb}")
     alpha_a, alpha_b = _tensor_scale(alpha_a, fmt, "alpha_a"), _tensor_scale(alpha_b, fmt, "alpha_b")
+    _fits_int32("beam_moe_gemm_fp4", m, n, k)
     out = _output(out, a_codes, (m, n), out_dtype or torch.bfloat16, stream)
     _call("beam_moe_gemm_fp4", _device_index(a_codes, a_sf, b_codes, b_sf, alpha_a, alpha_b, out), stream, form,
           a_codes.data_ptr(), lda, a_sf.data_ptr(), lda_sf, None if alpha_a is None else alpha_a.data_ptr(),

@@ -343,6 +343,9 @@ def test_refusals(bm):
                  lambda: bm.beam_moe_gemm_fp4(codes, sf, codes, sf, "nvfp4", out=torch.empty(4, 5, device="cuda"))):
         with pytest.raises(ValueError):
             call()
+    with pytest.raises(bm.BeamMoeError) as err:  # more rows than 32 bits count
+        bm.beam_moe_gemm_fp4(codes[:1].expand(2 ** 32 + 4, -1), sf[:1].expand(2 ** 32 + 4, -1), codes, sf, "nvfp4")
+    assert err.value.status == bm.ERR_UNSUPPORTED
     for call, status in ((lambda: bm.beam_moe_quantize_fp4(x[:, :48].contiguous(), "nvfp4"), bm.ERR_UNSUPPORTED),
                          (lambda: bm.beam_moe_quantize_fp4(x[:, 1:33], "mxfp4"), bm.ERR_INVALID_ARG),
                          # scale rows 4 bytes apart

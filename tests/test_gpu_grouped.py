@@ -320,6 +320,14 @@ def test_refusals(bm):
                  lambda: bm.beam_moe_grouped_gemm_wgrad(dy[:9], x, off)):
         with pytest.raises(ValueError):
             call()
+    # more rows than 32 bits count (one row of memory seen many times)
+    many = _draw((1, 32), BF16, 54).expand(2 ** 32 + 10, 32)
+    with pytest.raises(bm.BeamMoeError) as err:
+        bm.beam_moe_grouped_gemm(many, w, off)
+    assert err.value.status == bm.ERR_UNSUPPORTED
+    with pytest.raises(bm.BeamMoeError) as err:
+        bm.beam_moe_grouped_gemm_wgrad(many[:, :16], many, off)
+    assert err.value.status == bm.ERR_UNSUPPORTED
     wide = _draw((10, 34), BF16, 53)
     for call, status in ((lambda: bm.beam_moe_grouped_gemm(wide[:, 1:33], w, off), bm.ERR_INVALID_ARG),
                          (lambda: bm.beam_moe_grouped_gemm(wide[:, :32], w, off), bm.ERR_INVALID_ARG),
