@@ -84,3 +84,37 @@ def test_projections_in_4_bits_one_after_another(bm, fmt, tokens):
         acc = ((k + 15) // 16 * 2.0 ** -22 + 2.0 ** -21) * (a.abs() @ b.abs().t())
         assert bool(((nxt.double() - ref).abs() <= acc + 2.0 ** -8 * (ref.abs() + acc)).all())
         v = nxt
+
+
+@pytest.mark.parametrize("tokens", [4, 64])
+def test_a_layer_right_behind_the_operators(bm, tokens):
+    # x and the residual come out of the operators' last kernels, which let the layer's first one
+    # start early: the same bits as with the GPU waited for in between
+    import dataclasses
+
+    import moe_inputs as mi
+    from sparse_moe_layer_fp32_b200 import synthetic
+    shape = dataclasses.replace(mi.SHAPES["tiny"], tokens=tokens)
+    layer = synthetic.make_layer(shape, synthetic.make_weights(shape, 0, threads=2))
+    hidden = shape.hidden
+    w = bm.beam_moe_quantize_fp4(_draw((hidden, hidden), FP32, 20, 0.06), "mxfp4")
+    dense = _draw((1, hidden, hidden), BF16, 21, 0.06)
+    off = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+
+    def step(v, wait):
+        residual = bm.beam_moe_grouped_gemm(v, dense, off)
+        q = bm.beam_moe_quantize_fp4(v, "mxfp4")
+        x = bm.beam_moe_gemm_fp4(q[0], q[1], w[0], w[1], "mxfp4")
+        if wait:
+            torch.cuda.synchronize()
+        out = layer.forward(x, residual)
+        q = bm.beam_moe_quantize_fp4(out, "mxfp4")  # and an operator right behind the layer
+        return out, bm.beam_moe_dequantize_fp4(q[0], q[1], "mxfp4")
+
+    inputs = [_draw((tokens, hidden), BF16, 30 + i) for i in range(40)]
+    want = [step(v, True) for v in inputs]
+    torch.cuda.synchronize()
+    got = [step(v, False) for v in inputs]
+    layer.check()
+    assert all(torch.equal(a, b) for g, r in zip(got, want) for a, b in zip(g, r))
+    layer.close()
