@@ -70,6 +70,9 @@ __global__ void __launch_bounds__(256) router_gemv_kernel(const uint16_t* __rest
 constexpr int RBM = 64, RBN = 64, RBK = 32;
 
 // partial[split][T][E] = sum over this split's H range of x[t][h] * w[e][h]
+// x and w are loaded outside the read-only path: the kernel may have started before the one that
+// writes them (an operator on caller buffers, say) ended, and that path asks for memory that does
+// not change while the kernel runs.
 __global__ void __launch_bounds__(256) router_sgemm_kernel(const uint16_t* __restrict__ x,
                                                            const float* __restrict__ w, int T, int H, int E,
                                                            int k_per_split, float* __restrict__ partial) {
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(256) router_sgemm_kernel(const uint16_t* __res
     {  // x tile: 64 rows x 32 k, 8 BF16 per thread
       const int m = m0 + lrow;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (m < T) v = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * H + k0 + lk));
+      if (m < T) v = __ldcg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * H + k0 + lk));
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -101,8 +104,8 @@ __global__ void __launch_bounds__(256) router_sgemm_kernel(const uint16_t* __res
       float4 a = make_float4(0, 0, 0, 0), b = a;
       if (n < E) {
         const float4* p = reinterpret_cast<const float4*>(w + static_cast<size_t>(n) * H + k0 + lk);
-        a = __ldg(p);
-        b = __ldg(p + 1);
+        a = __ldcg(p);
+        b = __ldcg(p + 1);
       }
       Bs[lk + 0][lrow] = a.x; Bs[lk + 1][lrow] = a.y; Bs[lk + 2][lrow] = a.z; Bs[lk + 3][lrow] = a.w;
       Bs[lk + 4][lrow] = b.x; Bs[lk + 5][lrow] = b.y; Bs[lk + 6][lrow] = b.z; Bs[lk + 7][lrow] = b.w;

@@ -118,3 +118,35 @@ def test_a_layer_right_behind_the_operators(bm, tokens):
     layer.check()
     assert all(torch.equal(a, b) for g, r in zip(got, want) for a, b in zip(g, r))
     layer.close()
+
+
+@pytest.mark.parametrize("tokens,hidden,experts", [(9, 256, 16), (200, 5120, 256)])
+def test_routing_right_behind_the_operators(bm, tokens, hidden, experts):
+    # x comes out of an operator's kernel, which lets the router's first one (more than 8 tokens:
+    # the tiled product) start early: the same bits as with the GPU waited for in between
+    wr = _draw((experts, hidden), FP32, 50, hidden ** -0.5)
+    w = bm.beam_moe_quantize_fp4(_draw((hidden, 256), FP32, 51, 0.06), "nvfp4")
+    dense = _draw((1, hidden, 256), BF16, 52, 0.06)
+    off = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    inputs = [_draw((tokens, 256), BF16, 60 + i) for i in range(20)]
+
+    def step(v, wait):
+        out = []
+        for behind in ("4 bits", "grouped", "read back"):
+            q = bm.beam_moe_quantize_fp4(v, "nvfp4")
+            if behind == "4 bits":
+                x = bm.beam_moe_gemm_fp4(q[0], q[1], w[0], w[1], "nvfp4", alpha_a=q[2], alpha_b=w[2])
+            elif behind == "grouped":
+                x = bm.beam_moe_grouped_gemm(v, dense, off)
+            else:
+                q = bm.beam_moe_quantize_fp4(x, "nvfp4")
+                x = bm.beam_moe_dequantize_fp4(q[0], q[1], "nvfp4", alpha=q[2])
+            if wait:
+                torch.cuda.synchronize()
+            out += bm.beam_moe_route(x, wr, 2)
+        return out
+
+    want = [step(v, True) for v in inputs]
+    torch.cuda.synchronize()
+    got = [step(v, False) for v in inputs]
+    assert all(torch.equal(a, b) for g, r in zip(got, want) for a, b in zip(g, r))
