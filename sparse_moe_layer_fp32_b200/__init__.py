@@ -32,7 +32,7 @@ EXPORTED = [
     "beam_moe_forward_ep_phase", "beam_moe_set_router_mode", "beam_moe_set_tp_two_shot_tokens",
     "beam_moe_set_host_chunk_tokens", "beam_moe_grouped_gemm", "beam_moe_grouped_gemm_dgrad",
     "beam_moe_grouped_gemm_wgrad", "beam_moe_check_operators", "beam_moe_quantize_fp4", "beam_moe_dequantize_fp4",
-    "beam_moe_gemm_fp4",
+    "beam_moe_gemm_fp4", "beam_moe_debug_operators_timeout",
 ]
 IPC_HANDLE_BYTES = 64
 FMT_NVFP4, FMT_MXFP8 = 0, 1
@@ -115,6 +115,7 @@ def _load():
         "beam_moe_grouped_gemm_dgrad": (i32, [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, i32, vp]),
         "beam_moe_grouped_gemm_wgrad": (i32, [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, i32, vp]),
         "beam_moe_check_operators": (i32, [vp]),
+        "beam_moe_debug_operators_timeout": (i32, [i64, vp, vp]),
         "beam_moe_quantize_fp4": (i32, [i32, vp, i32, i64, i64, i32, f32, vp, i64, vp, i64, vp, vp]),
         "beam_moe_dequantize_fp4": (i32, [i32, vp, i64, vp, i64, vp, i64, i32, vp, i32, i64, vp]),
         "beam_moe_gemm_fp4": (i32, [i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32, i32, vp, i32, i64, vp]),
@@ -579,6 +580,12 @@ def beam_moe_check_operators(device=None, stream=None):
     """Waits for `stream` and raises if an operator on `device` gave up a wait since the last check."""
     with torch.cuda.device(device):
         _check(_lib.beam_moe_check_operators(_stream(stream)), "beam_moe_check_operators")
+
+
+def beam_moe_debug_operators_timeout(limit_ns: int, result, stream=None):
+    """Runs the operators' bounded wait into its limit; result: int32 tensor on the current device."""
+    _check(_lib.beam_moe_debug_operators_timeout(int(limit_ns), _ptr(result), _stream(stream)),
+           "beam_moe_debug_operators_timeout")
 
 
 # ------------------------------------------------------------------ handle wrapper

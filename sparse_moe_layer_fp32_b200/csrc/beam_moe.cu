@@ -998,14 +998,6 @@ beam_moe_status beam_moe_debug_copy(beam_moe_t h, int32_t which, void* dst, size
   return BEAM_MOE_OK;
 }
 
-beam_moe_status beam_moe_check_operators(void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t grouped = 0, fp4 = 0;
-  BEAM_TRY(take_grouped_gemm_errors(&grouped, s));
-  BEAM_TRY(take_gemm_fp4_errors(&fp4, s));
-  return (grouped | fp4) ? BEAM_MOE_ERR_TIMEOUT : BEAM_MOE_OK;
-}
-
 beam_moe_status beam_moe_check(beam_moe_t h, void* stream) {
   if (!h) return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -84,12 +84,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait (kWaitLimitNs): false, with *abort_flag set, once the wait ran past the limit or
-// another role gave up.  The clock is first read after kQuietTries tries (each suspends the
+// Bounded wait: false, with *abort_flag set, once the wait ran past the limit or another role gave
+// up.  The clock is first read after kQuietTries tries (each suspends the
 // thread for a while): reading %globaltimer takes about a microsecond, which on every wait that
 // did not succeed at once held a ring stage to ~800 cycles.
 constexpr uint32_t kQuietTries = 256;
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t limit_ns = kWaitLimitNs) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -97,7 +98,7 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volati
       if (*abort_flag) return false;
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) {
+      if (t - t0 > limit_ns) {
         *abort_flag = 1;
         return false;
       }

@@ -533,7 +533,9 @@ bool on(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
-cudaError_t take_gemm_fp4_errors(uint32_t* bits, cudaStream_t s) { return take_error_word(g_fp4_err, bits, s); }
+cudaError_t gemm_fp4_error_word(uint32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_fp4_err);
+}
 
 }  // namespace beam
 

@@ -547,8 +547,8 @@ cudaError_t launch_grouped_gemm(int mode, const void* rows_a, int64_t ld_a, cons
   return launch_out<kWgrad>(out_type, a, ma, mb, mb2, tiles, s);
 }
 
-cudaError_t take_grouped_gemm_errors(uint32_t* bits, cudaStream_t s) {
-  return take_error_word(g_grouped_err, bits, s);
+cudaError_t grouped_gemm_error_word(uint32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_grouped_err);
 }
 
 }  // namespace beam

@@ -247,21 +247,12 @@ cudaError_t launch_finalize(const uint16_t* y, const float* w, const int32_t* in
                             const uint16_t* next_gamma, float next_eps, uint32_t* err, cudaStream_t s,
                             int form_T = 0);
 
-// ---- operators on caller buffers (grouped_gemm.cu, gemm_fp4.cu, quant_fp4.cu)
+// ---- operators on caller buffers (grouped_gemm.cu, gemm_fp4.cu, quant_fp4.cu, operators.cu)
 constexpr int kTypeBf16 = BEAM_MOE_BF16, kTypeFp16 = BEAM_MOE_FP16, kTypeFp32 = BEAM_MOE_FP32;
 // cuTensorMapEncodeTiled, or nullptr where the driver has none (beam_moe.cu).
 void* tensor_map_encode_fn();
-// Error bits that this device's operators have set since the last call; synchronises s.
-cudaError_t take_grouped_gemm_errors(uint32_t* bits, cudaStream_t s);
-cudaError_t take_gemm_fp4_errors(uint32_t* bits, cudaStream_t s);
-template <class Symbol>
-cudaError_t take_error_word(Symbol& word, uint32_t* bits, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(bits, word, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess || *bits == 0) return e;
-  static const uint32_t zero = 0;
-  e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
-}
+// Address of the current device's error word of these kernels.
+cudaError_t grouped_gemm_error_word(uint32_t** word);
+cudaError_t gemm_fp4_error_word(uint32_t** word);
 
 }  // namespace beam

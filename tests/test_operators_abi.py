@@ -142,3 +142,11 @@ def test_tensors_have_to_be_on_a_gpu():
         bm.beam_moe_grouped_gemm(x, w, off)
     with pytest.raises(ValueError):
         bm.beam_moe_grouped_gemm_wgrad(x, x, off)
+
+
+def test_debug_timeout():
+    call = bm.lib().beam_moe_debug_operators_timeout
+    assert call(0, P, None) == BAD
+    assert call(2 * 10**9 + 1, P, None) == BAD
+    assert call(10**6, None, None) == BAD
+    assert call(10**6, P + 2, None) == BAD
