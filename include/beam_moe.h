@@ -415,9 +415,11 @@ BEAM_MOE_API beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_
  * in one step in the order of `stream`, and synchronises `stream`.  Returns OK or TIMEOUT: a wait
  * gave up since the last check, and the outputs of the call that it belongs to are not complete. */
 BEAM_MOE_API beam_moe_status beam_moe_check_operators(void* stream);
-/* Test support: runs the operators' bounded wait, with a limit of limit_ns (up to 2 s), into its
- * limit on `stream`.  result (device int32): [0] 1 where the wait gave up and told its CTA.  The
- * error words are set as by the operators, so that the next check returns TIMEOUT. */
+/* Test support: runs the operators' bounded wait, with a limit of limit_ns (up to 0.5 s), into its
+ * limit on `stream`.  result (device int32 [3]): [0] 1 where the wait gave up and told its CTA; then
+ * two CTAs hand sums over as in a tile that several pairs share: [1] 1 where a sender that gave up
+ * released the receiver, [2] 1 where a receiver that gave up stayed until a late sender's sums had
+ * landed.  The error words are set as by the operators, so that the next check returns TIMEOUT. */
 BEAM_MOE_API beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* result, void* stream);
 
 /* Internal buffers of the last forward, for tests (layouts in the comment of each id). */

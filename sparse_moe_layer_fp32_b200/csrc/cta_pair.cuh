@@ -60,6 +60,11 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
                : "memory");
 }
 
+// Counts `bytes` as received at a barrier of another CTA, for a copy that will not be made.
+__device__ __forceinline__ void mbar_complete_tx_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Arrivals at a barrier of either CTA (address from map_to_cta).  Plain: releases this thread's
 // accesses to its own CTA only, which is right where what it announces are finished TMEM accesses
 // or shared memory behind a proxy fence, both used only by the own SM's tensor core.  The relaxed
@@ -104,6 +109,28 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
+}
+
+// The sums of a tile that several pairs share, on their way to the CTA that adds them up.  A sender
+// whose own sums did not come (!ok) counts them as received all the same; one thread calls.
+__device__ __forceinline__ void send_sums(bool ok, uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  if (ok)
+    bulk_copy_to_cta(to, from, bytes, bar);
+  else
+    mbar_complete_tx_at(bar, bytes);
+}
+// Whether this CTA's own sums (ok) and every sender's have come; whole warps call.  No sender's copy
+// may find this CTA gone.  A sender decides within one wait limit of its start, the CTAs of a
+// cluster start together, and a role here gives up one limit after that at the earliest: whoever
+// gives up holds this CTA for another limit, unless all that will come has come before.
+__device__ __forceinline__ bool receive_sums(bool ok, uint64_t* bar, volatile int* abort_flag,
+                                             uint64_t limit_ns = kWaitLimitNs) {
+  if (ok && __all_sync(0xffffffffu, pair_wait(bar, 0, abort_flag, limit_ns))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+  }
+  __syncwarp();
+  return false;
 }
 
 // Tiled TMA loads into this CTA, completing on a barrier of either CTA of the pair.

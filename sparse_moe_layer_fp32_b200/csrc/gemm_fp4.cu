@@ -385,10 +385,10 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
       }
       fence_proxy_async_smem();
       asm volatile("bar.sync 1, %0;" ::"n"(32 * F4_EPI_WARPS) : "memory");
-      if (ok && warp == F4_FIRST_EPI && lane == 0)
-        bulk_copy_to_cta(map_to_cta(tail->sums + (pair - 1) * rows * 128, rank), smem, static_cast<uint32_t>(rows) * 512,
-                         map_to_cta(&tail->sums_full, rank));
-    } else if (ok && __all_sync(0xffffffffu, pair_wait(&tail->sums_full, 0, abort_flag))) {
+      if (warp == F4_FIRST_EPI && lane == 0)
+        send_sums(ok, map_to_cta(tail->sums + (pair - 1) * rows * 128, rank), smem, static_cast<uint32_t>(rows) * 512,
+                  map_to_cta(&tail->sums_full, rank));
+    } else if (receive_sums(ok, &tail->sums_full, abort_flag)) {
       for (int c = part * 2; c < rows; c += 8) {
         uint32_t v[2];
         tmem_ld_32x32b_x2(from + c, v);

@@ -40,6 +40,50 @@ __global__ void operators_timeout_probe_kernel(uint64_t limit_ns, uint32_t* grou
   }
 }
 
+// A cluster of two CTAs hands sums over as the pairs of a shared tile do.
+//   late: the receiver has given up, the sender sends two limits later: the receiver must still be
+//         there when the sums land (result: they had, and it reports that it gave up);
+//   else: the sender's own wait gives up: the receiver is released by it, well before its own limit.
+constexpr uint32_t kProbeWords = 512;
+__global__ void sums_probe_kernel(uint64_t limit_ns, int late, int32_t* result) {
+  __shared__ alignas(16) uint32_t sums[kProbeWords];
+  __shared__ uint64_t bar, never;
+  __shared__ int abort_flag;
+  const uint32_t rank = cluster_cta_rank();
+  pdl_wait();
+  for (uint32_t i = threadIdx.x; i < kProbeWords; i += blockDim.x) sums[i] = rank == 0 ? 0u : i + 1;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    mbar_init(&never, 1);
+    abort_flag = rank == 0 && late;
+    if (rank == 0) mbar_arrive_expect_tx(&bar, kProbeWords * 4);
+    fence_mbar_init();
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  cluster_sync();
+  if (rank == 1) {
+    bool ok = late != 0;
+    if (late) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2 * limit_ns) __nanosleep(1000);
+    } else {
+      ok = __all_sync(0xffffffffu, pair_wait(&never, 0, &abort_flag, limit_ns));
+    }
+    __syncwarp();
+    if (threadIdx.x == 0) send_sums(ok, map_to_cta(sums, 0), sums, kProbeWords * 4, map_to_cta(&bar, 0));
+  } else {
+    const bool got = receive_sums(!late, &bar, &abort_flag, kWaitLimitNs);
+    bool right = got != (late != 0);
+    if (late)
+      for (uint32_t i = threadIdx.x; i < kProbeWords; i += blockDim.x) right = right && sums[i] == i + 1;
+    right = __all_sync(0xffffffffu, right);
+    if (threadIdx.x == 0) *result = right;
+  }
+  __syncwarp();
+  cluster_sync();
+}
+
 }  // namespace
 
 }  // namespace beam
@@ -64,7 +108,7 @@ beam_moe_status beam_moe_check_operators(void* stream) {
 }
 
 beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* result, void* stream) {
-  if (limit_ns <= 0 || limit_ns > static_cast<int64_t>(kWaitLimitNs) || !result ||
+  if (limit_ns <= 0 || limit_ns > static_cast<int64_t>(kWaitLimitNs / 4) || !result ||
       (reinterpret_cast<uintptr_t>(result) & 3))
     return BEAM_MOE_ERR_INVALID_ARG;
   uint32_t *grouped = nullptr, *fp4 = nullptr;
@@ -73,7 +117,11 @@ beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* resu
   if (e != cudaSuccess) return BEAM_MOE_ERR_CUDA;
   operators_timeout_probe_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint64_t>(limit_ns),
                                                                                   grouped, fp4, result);
-  return cudaGetLastError() == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA;
+  e = cudaGetLastError();
+  for (int late = 0; late < 2 && e == cudaSuccess; ++late)
+    e = launch_pdl_clusters(sums_probe_kernel, 2, 2, 32, 0, static_cast<cudaStream_t>(stream),
+                            static_cast<uint64_t>(limit_ns), late, result + 1 + late);
+  return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -32,6 +32,21 @@ def test_a_wait_that_gives_up_is_reported_once(bm):
         bm.beam_moe_check_operators()
 
 
+def test_a_shared_tiles_sums_where_a_side_gives_up(bm):
+    result = torch.zeros(4, dtype=torch.int32, device="cuda")
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    bm.beam_moe_debug_operators_timeout(LIMIT, result)
+    end.record()
+    torch.cuda.synchronize()
+    assert result.tolist() == [1, 1, 1, 0]
+    # three waits of one or two limits each: none ran into the 2 s limit
+    assert start.elapsed_time(end) < 1000
+    with pytest.raises(bm.BeamMoeError):
+        bm.beam_moe_check_operators()
+    bm.beam_moe_check_operators()
+
+
 def test_a_check_on_another_stream_takes_what_is_there(bm):
     # every report is given by one check and no report is lost, whichever streams ask
     streams = [torch.cuda.Stream() for _ in range(2)]

@@ -147,6 +147,6 @@ def test_tensors_have_to_be_on_a_gpu():
 def test_debug_timeout():
     call = bm.lib().beam_moe_debug_operators_timeout
     assert call(0, P, None) == BAD
-    assert call(2 * 10**9 + 1, P, None) == BAD
+    assert call(5 * 10**8 + 1, P, None) == BAD
     assert call(10**6, None, None) == BAD
     assert call(10**6, P + 2, None) == BAD
