@@ -354,7 +354,8 @@ BEAM_MOE_API beam_moe_status beam_moe_quantize_mxfp8(const float* src, int64_t r
  *   - The tensor cores' FP32 accumulation truncates: a long sum loses about 1e-9 of its
  *     magnitude per term (5e-6 relative over 4096 terms), which only FP32 outputs show.
  *   - No workspace, no state: calls on different streams may overlap.
- * The device side waits are bounded (2 s); beam_moe_check_operators reports one that gave up. */
+ * The device side waits are bounded (2 s without progress: a sum itself may take longer);
+ * beam_moe_check_operators reports one that gave up. */
 enum { BEAM_MOE_BF16 = 0, BEAM_MOE_FP16 = 1, BEAM_MOE_FP32 = 2 };
 BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w, const int32_t* offsets,
                                                    int32_t rows, int32_t groups, int32_t n, int32_t k, int32_t type,
@@ -416,10 +417,10 @@ BEAM_MOE_API beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_
  * gave up since the last check, and the outputs of the call that it belongs to are not complete. */
 BEAM_MOE_API beam_moe_status beam_moe_check_operators(void* stream);
 /* Test support: runs the operators' bounded wait, with a limit of limit_ns (up to 0.5 s), into its
- * limit on `stream`.  result (device int32 [3]): [0] 1 where the wait gave up and told its CTA; then
- * two CTAs hand sums over as in a tile that several pairs share: [1] 1 where a sender that gave up
+ * limit on `stream`.  result (device int32 [4]): [0] 1 where the wait gave up and told its CTA; two CTAs hand sums over as in a tile that several pairs share: [1] 1 where a sender that gave up
  * released the receiver, [2] 1 where a receiver that gave up stayed until a late sender's sums had
- * landed.  The error words are set as by the operators, so that the next check returns TIMEOUT. */
+ * landed; [3] 1 where a wait of three limits was met because the role before it made progress, and
+ * one without progress was not.  The error words are set as by the operators, so that the next check returns TIMEOUT. */
 BEAM_MOE_API beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* result, void* stream);
 
 /* Internal buffers of the last forward, for tests (layouts in the comment of each id). */

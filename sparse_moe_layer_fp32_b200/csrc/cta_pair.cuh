@@ -93,16 +93,25 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // up.  The clock is first read after kQuietTries tries (each suspends the
 // thread for a while): reading %globaltimer takes about a microsecond, which on every wait that
 // did not succeed at once held a ring stage to ~800 cycles.
+// A role that waits for more than a stage of the ring (a whole sum, which may rightly take longer
+// than the limit) passes `progress`, a word of this CTA's shared memory that the loading warp
+// changes with every stage: the limit then counts from its last change.
 constexpr uint32_t kQuietTries = 256;
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          uint64_t limit_ns = kWaitLimitNs) {
+                                          uint64_t limit_ns = kWaitLimitNs,
+                                          const volatile uint32_t* progress = nullptr) {
   uint64_t t0 = 0;
+  uint32_t seen = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (i % kQuietTries == 0) {
       if (*abort_flag) return false;
       const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
+      const uint32_t at = progress ? *progress : 0u;
+      if (t0 == 0 || at != seen) {
+        t0 = t;
+        seen = at;
+      }
       if (t - t0 > limit_ns) {
         *abort_flag = 1;
         return false;

@@ -64,6 +64,7 @@ constexpr int F4_SF_STAGE = 48;                 // M: 4 columns per K group, the
 constexpr int F4_SF_N = 16;
 static_assert(F4_SF_COL + F4_STAGES * F4_SF_STAGE <= 512, "scales fit in TMEM");
 constexpr int F4_MAX_SPLIT = 4;                 // pairs that share a tile
+constexpr int F4_MAX_SHARE = 1 << 20;           // stages of a pair's share: 0.3 us each, far below the wait limit
 constexpr int F4_SUM_ROWS = 64;                 // rows of sums that a shared tile's first pair can receive
 constexpr int F4_FIRST_SF = 4, F4_FIRST_EPI = 8, F4_EPI_WARPS = 16;
 constexpr int F4_THREADS = 32 * (F4_FIRST_EPI + F4_EPI_WARPS);
@@ -88,6 +89,7 @@ struct __align__(16) Fp4Tail {
   uint64_t sums_full;            // shared tiles: the other pairs' sums have come
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t progress;             // stages loaded
   alignas(16) float sums[F4_SUM_ROWS * 128];  // shared tiles: received sums
 };
 constexpr size_t kFp4Smem = static_cast<size_t>(F4_STAGES) * F4_STAGE + sizeof(Fp4Tail) + 1024;
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Fp4Tail* tail = reinterpret_cast<Fp4Tail*>(smem + F4_STAGES * F4_STAGE);
   volatile int* abort_flag = &tail->abort_flag;
+  volatile uint32_t* progress = &tail->progress;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cluster_rank = cluster_cta_rank();
   const uint32_t rank = cluster_rank & 1;                        // in the pair
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     if (kSplit && pair == 0)
       mbar_arrive_expect_tx(&tail->sums_full, static_cast<uint32_t>((args.split - 1) * args.m) * 512);
     tail->abort_flag = 0;
+    tail->progress = 0;
     fence_mbar_init();
   }
   if (warp == 3) {
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, loaded = 0;
     bool ok = true;
     const uint32_t code_bytes = F4_CODES + static_cast<uint32_t>(args.height) * (128 / 2);
     const uint32_t sf_bytes = 128 * 16 + static_cast<uint32_t>(args.height) * 16;
@@ -206,7 +210,9 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
       for (int i = step0; i < step1; ++i) {
         ok = __all_sync(0xffffffffu, pair_wait(&tail->empty[stage], phase ^ 1, abort_flag));
         if (!ok) break;
+        ++loaded;
         if (elect_one()) {
+          *progress = loaded;
           uint8_t* s = smem + stage * F4_STAGE;
           uint64_t* bar = &tail->full[stage];
           // 16 scale bytes of a row: this K step's (NVFP4), or those of an even step and the next,
@@ -365,6 +371,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;
     const float scale = (args.alpha_a ? __ldcg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldcg(args.alpha_b) : 1.0f);
     const Fp4Tile t = fp4_tile(args, first_tile);
+    // the whole sum within one limit, which receive_sums counts on: at most F4_MAX_SHARE stages
     const bool ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_full, 0, abort_flag));
     tc_fence_after();
     const int rows = t.r_end - t.r0, slot = quarter * 32 + lane;
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
     uint32_t acc_phase = 0;
     for (int id = first_tile; id < total; id += tile_stride) {
       const Fp4Tile t = fp4_tile(args, id);
-      if (!__all_sync(0xffffffffu, pair_wait(&tail->acc_full, acc_phase, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, pair_wait(&tail->acc_full, acc_phase, abort_flag, kWaitLimitNs, progress))) break;
       acc_phase ^= 1;
       tc_fence_after();
       const int c0 = part * 64;
@@ -511,11 +518,12 @@ cudaError_t launch_fp4(Fp4Args a, const Fp4Maps& maps, cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(a.blocks) * ((a.n + F4_TILE - 1) / F4_TILE);
   // As many pairs to a tile of one row block as leave no SM idle, as far as the first can receive
   // their sums, in clusters of up to eight CTAs, and each with a ring's worth of K steps at least:
-  // the exchange takes as long as those.
+  // the exchange takes as long as those.  A longer share than F4_MAX_SHARE is not waited for in one
+  // piece: such a tile is left to one pair.
   const int64_t steps = (a.k + F4_BK - 1) / F4_BK;
   const int64_t fit = a.blocks == 1 ? 1 + F4_SUM_ROWS / a.m : 1;
   a.split = static_cast<int>(std::min({int64_t{F4_MAX_SPLIT}, sms / 2 / tiles, steps / F4_STAGES, fit}));
-  if (a.split > 1)
+  if (a.split > 1 && (steps + a.split - 1) / a.split <= F4_MAX_SHARE)
     return launch_fp4_as<FORMAT, OUT, true>(a, maps, static_cast<unsigned>(tiles * 2 * a.split),
                                             static_cast<unsigned>(2 * a.split), s);
   a.split = 1;

@@ -96,6 +96,7 @@ struct __align__(16) GroupedTail {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t progress;              // stages loaded
   int total_tiles;
   int begin[GG_MAX_GROUPS + 1];   // clamped offsets
   int first[GG_MAX_GROUPS + 1];   // first tile of each group
@@ -158,6 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   GroupedTail* tail = reinterpret_cast<GroupedTail*>(smem + GG_STAGES * GG_STAGE);
   volatile int* abort_flag = &tail->abort_flag;
+  volatile uint32_t* progress = &tail->progress;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
 
@@ -175,6 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
     }
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
+    tail->progress = 0;
     fence_mbar_init();
   }
   if (warp == 3) {
@@ -231,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, loaded = 0;
     bool ok = true;
     for (int id = first_tile; id < total && ok; id += tile_stride) {
       const GroupedTile t = grouped_tile<MODE>(args, tail, id);
@@ -249,7 +252,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         const int step = i * GG_BK;
         // a ragged stage lands on this CTA's own barrier; warp 2 hands it on
         const bool ragged = MODE == kWgrad && i == t.steps - 1 && (length & 15) != 0;
+        ++loaded;
         if (elect_one()) {
+          *progress = loaded;
           const uint32_t bar = ragged ? map_to_cta(&tail->landed[stage], rank) : map_to_cta(&tail->full[stage], 0);
           mbar_arrive_expect_tx_relaxed_at(bar, bytes);
           if (MODE == kFwd) {
@@ -357,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
         stage = (stage + t.steps) % GG_STAGES;
         const int rows = tail->begin[t.group + 1] - tail->begin[t.group] - (t.steps - 1) * GG_BK;
         if ((rows & 15) == 0) continue;
-        ok = pair_wait(&tail->landed[last], (parity >> last) & 1u, abort_flag);
+        ok = pair_wait(&tail->landed[last], (parity >> last) & 1u, abort_flag, kWaitLimitNs, progress);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         parity ^= 1u << last;
@@ -391,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
       const GroupedTile t = grouped_tile<MODE>(args, tail, id);
       const bool any = t.steps > 0;
       if (any) {
-        ok = ok && __all_sync(0xffffffffu, pair_wait(&tail->acc_full[acc], acc_phase, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, pair_wait(&tail->acc_full[acc], acc_phase, abort_flag, kWaitLimitNs, progress));
         tc_fence_after();
       }
       const int m = t.m0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;

@@ -19,13 +19,18 @@ __global__ void take_errors_kernel(uint32_t* grouped, uint32_t* fp4) {
   g_taken = atomicExch(grouped, 0u) | atomicExch(fp4, 0u);
 }
 
-// One CTA waits, with the operators' bounded wait, at a barrier that nothing completes.
+// One CTA waits, with the operators' bounded wait, at a barrier that nothing completes (result[0]).
+// Then its second warp waits at a barrier that the first completes after three limits, making
+// progress in between, and once more, without progress, at the other one (result[3]: met, not met).
 __global__ void operators_timeout_probe_kernel(uint64_t limit_ns, uint32_t* grouped, uint32_t* fp4, int32_t* result) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, later;
   __shared__ int abort_flag;
+  __shared__ uint32_t progress;
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
+    mbar_init(&later, 1);
     abort_flag = 0;
+    progress = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -37,6 +42,19 @@ __global__ void operators_timeout_probe_kernel(uint64_t limit_ns, uint32_t* grou
       atomicOr(grouped, kErrTimeoutMma);
       atomicOr(fp4, kErrTimeoutMma);
     }
+    abort_flag = 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 1; i <= 12; ++i) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < limit_ns / 4) __nanosleep(1000);
+      *static_cast<volatile uint32_t*>(&progress) = i;
+    }
+    mbar_arrive_at(map_to_cta(&later, 0));
+  } else if (threadIdx.x == 32) {
+    const bool met = pair_wait(&later, 0, &abort_flag, limit_ns, &progress);
+    result[3] = met && !pair_wait(&bar, 0, &abort_flag, limit_ns, &progress) && abort_flag;
   }
 }
 
@@ -115,7 +133,7 @@ beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* resu
   cudaError_t e = grouped_gemm_error_word(&grouped);
   if (e == cudaSuccess) e = gemm_fp4_error_word(&fp4);
   if (e != cudaSuccess) return BEAM_MOE_ERR_CUDA;
-  operators_timeout_probe_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint64_t>(limit_ns),
+  operators_timeout_probe_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint64_t>(limit_ns),
                                                                                   grouped, fp4, result);
   e = cudaGetLastError();
   for (int late = 0; late < 2 && e == cudaSuccess; ++late)

@@ -39,12 +39,69 @@ def test_a_shared_tiles_sums_where_a_side_gives_up(bm):
     bm.beam_moe_debug_operators_timeout(LIMIT, result)
     end.record()
     torch.cuda.synchronize()
-    assert result.tolist() == [1, 1, 1, 0]
-    # three waits of one or two limits each: none ran into the 2 s limit
+    assert result[:3].tolist() == [1, 1, 1]
+    # waits of a few limits each: none ran into the 2 s limit
     assert start.elapsed_time(end) < 1000
     with pytest.raises(bm.BeamMoeError):
         bm.beam_moe_check_operators()
     bm.beam_moe_check_operators()
+
+
+def test_the_limit_counts_from_the_last_progress(bm):
+    result = torch.zeros(4, dtype=torch.int32, device="cuda")
+    bm.beam_moe_debug_operators_timeout(LIMIT, result)
+    assert result[3].item() == 1
+    with pytest.raises(bm.BeamMoeError):
+        bm.beam_moe_check_operators()
+
+
+def test_a_sum_longer_than_the_limit(bm):
+    # one tile's sum over 2^30 - 1 rows takes longer than the waits' 2 s.  Rows of +-1, each times the
+    # row behind it: the sums walk within +-2^20 and are exact in FP32
+    rows = 2 ** 30
+    buf = torch.empty((rows, 8), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    step = 1 << 22
+    for i in range(0, rows, step):
+        buf[i:i + step] = torch.randint(0, 2, (step, 8), generator=g, device="cuda") * 2 - 1
+    dy, x = buf[:-1], buf[1:]
+    off = torch.tensor([0, rows - 1], dtype=torch.int32, device="cuda")
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    dw = bm.beam_moe_grouped_gemm_wgrad(dy, x, off, out_dtype=torch.float32)
+    end.record()
+    bm.beam_moe_check_operators()
+    print(f"sum over {rows - 1} rows: {start.elapsed_time(end):.0f} ms")
+    ref = torch.zeros((8, 8), dtype=torch.float64, device="cuda")
+    for i in range(0, rows - 1, step):
+        ref += (dy[i:i + step].float().t() @ x[i:i + step].float()).double()  # whole numbers below 2^24
+    assert torch.equal(dw[0].double(), ref)
+
+
+@pytest.mark.parametrize("k", [2 ** 29 + 96, 2 ** 30 + 2 ** 20 + 32])
+def test_a_product_of_long_rows(bm, k):
+    # few tiles and long sums: as long as pairs that share a tile wait for, and longer.  Codes of +-1:
+    # the sums walk within +-2^20 and are exact in FP32
+    n = 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+
+    def matrix(rows):
+        codes = torch.empty((rows, (k // 2 + 15) // 16 * 16), dtype=torch.uint8, device="cuda")
+        for r in range(rows):
+            codes[r] = torch.randint(0, 256, (codes.shape[1],), generator=g, device="cuda", dtype=torch.uint8)
+        codes.bitwise_and_(0x88).bitwise_or_(0x22)
+        sf = torch.full((rows, (k // 32 + 15) // 16 * 16), 127, dtype=torch.uint8, device="cuda")
+        return codes[:, :k // 2], sf[:, :k // 32]
+
+    a, b = matrix(1), matrix(n)
+    out = bm.beam_moe_gemm_fp4(a[0], a[1], b[0], b[1], "mxfp4", out_dtype=torch.float32)
+    bm.beam_moe_check_operators()
+    for j in range(n):
+        signs = a[0][0] ^ b[0][j]
+        minus = sum(int(((part >> bit) & 1).sum()) for part in signs.split(1 << 26) for bit in (3, 7))
+        assert out[0, j].item() == k - 2 * minus
 
 
 def test_a_check_on_another_stream_takes_what_is_there(bm):
