@@ -384,8 +384,8 @@ BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t
 enum { BEAM_MOE_FP4_MX = 0, BEAM_MOE_FP4_NV = 1 };
 
 /* src [rows][cols] of src_type (BF16, FP16 or FP32), rows ld elements apart (a multiple of 16
- * bytes).  alpha and alpha_out as in beam_moe_quantize_nvfp4: alpha > 0 is NVFP4's tensor scale;
- * alpha <= 0 takes the largest finite |src| / 2688, found on the device.  alpha_out (device
+ * bytes).  alpha and alpha_out as in beam_moe_quantize_nvfp4: alpha > 0 is NVFP4's tensor scale
+ * (infinity and NaN are INVALID_ARG); alpha <= 0 takes the largest finite |src| / 2688, found on the device.  alpha_out (device
  * FP32; may be NULL where alpha > 0) receives the scale used.  MXFP4 uses neither.  A block that
  * holds a NaN or an infinity gets a NaN scale and zero codes: it reads back, and multiplies, as
  * NaN. */

@@ -522,8 +522,9 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     kind = TYPES.get(src.dtype)
     if kind is None:
         raise ValueError("src has to be BF16, FP16 or FP32")
-    if alpha is not None and not 0.0 < alpha < float("inf"):
-        raise ValueError("alpha has to be a positive finite number")
+    # as the library gets it: a positive number that rounds to 0 would ask it to find the scale
+    if alpha is not None and not 0.0 < ctypes.c_float(alpha).value < float("inf"):
+        raise ValueError("alpha has to be a positive finite FP32 number")
     ld = _row_stride(src, "src")
     rows, cols = src.shape
     _fits_int32("beam_moe_quantize_fp4", cols)

@@ -448,7 +448,7 @@ beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t s
     return BEAM_MOE_ERR_INVALID_ARG;
   const bool nv = format == BEAM_MOE_FP4_NV;
   const bool given = alpha > 0.0f && alpha <= 3.4028235e38f;
-  if (nv && !given && (alpha > 0.0f || !alpha_out)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (nv && !given && (!(alpha <= 0.0f) || !alpha_out)) return BEAM_MOE_ERR_INVALID_ARG;  // infinite, NaN
   if (nv && alpha_out && !aligned_to(alpha_out, 4)) return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const float* amax = nullptr;

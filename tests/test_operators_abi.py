@@ -104,6 +104,7 @@ def test_fp4_quantiser():
     assert _quantize(form=bm.FP4_NV, alpha=0.0) == BAD             # nowhere to put the scale found
     assert _quantize(form=bm.FP4_NV, alpha=float("inf")) == BAD
     assert _quantize(form=bm.FP4_NV, alpha_out=P + 2) == BAD
+    assert _quantize(form=bm.FP4_NV, alpha=float("nan"), alpha_out=P) == BAD  # not "find the scale"
 
 
 def test_fp4_product():
@@ -150,3 +151,14 @@ def test_debug_timeout():
     assert call(5 * 10**8 + 1, P, None) == BAD
     assert call(10**6, None, None) == BAD
     assert call(10**6, P + 2, None) == BAD
+
+
+def test_tensor_scales_that_single_precision_does_not_hold():
+    # they would reach the library as 0 ("find the scale") or infinity
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for alpha in (1e-46, 7e-46, 5e-324, 3.5e38, 1e39):
+        with pytest.raises(ValueError, match="alpha"):
+            bm.beam_moe_quantize_fp4(x, "nvfp4", alpha=alpha)
+    for alpha in (8e-46, 1e-45, 3.4e38):  # the smallest and the largest pass to the next check
+        with pytest.raises(ValueError, match="device"):
+            bm.beam_moe_quantize_fp4(x, "nvfp4", alpha=alpha)
