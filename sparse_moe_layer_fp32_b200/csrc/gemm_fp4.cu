@@ -115,6 +115,21 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& a, int id) {
   return t;
 }
 
+// The two tensor scales: `scale` is their product, and `first` 1, wherever the product is a normal
+// number.  Where it is not (1e-23 and 1e-23, say, with sums around 1e10) a sum takes the larger scale
+// first and then the smaller, which leaves the normal range only where the result does.
+struct TensorScales {
+  float first, scale;
+};
+__device__ __forceinline__ TensorScales tensor_scales(const float* alpha_a, const float* alpha_b) {
+  const float a = alpha_a ? __ldcg(alpha_a) : 1.0f, b = alpha_b ? __ldcg(alpha_b) : 1.0f;
+  const float p = a * b;
+  const bool plain = (fabsf(p) >= 0x1p-126f && fabsf(p) < INFINITY) || a == 0.0f || b == 0.0f ||
+                     !(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY);
+  if (plain) return {1.0f, p};
+  return fabsf(a) >= fabsf(b) ? TensorScales{a, b} : TensorScales{b, a};
+}
+
 template <int FORMAT>
 __device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t leader) {
@@ -369,7 +384,8 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   } else if (kSplit && warp >= F4_FIRST_EPI) {
     // ------------------------------------------------------------ results of a shared tile
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;
-    const float scale = (args.alpha_a ? __ldcg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldcg(args.alpha_b) : 1.0f);
+    const TensorScales by = tensor_scales(args.alpha_a, args.alpha_b);
+    const float scale = by.scale;
     const Fp4Tile t = fp4_tile(args, first_tile);
     // the whole sum within one limit, which receive_sums counts on: at most F4_MAX_SHARE stages
     const bool ok = __all_sync(0xffffffffu, pair_wait(&tail->acc_full, 0, abort_flag));
@@ -407,6 +423,7 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
 #pragma unroll
           for (int q = 0; q < F4_MAX_SPLIT - 1; ++q)
             if (q < args.split - 1) sum += tail->sums[(q * rows + c + j) * 128 + slot];
+          sum *= by.first;
           const int64_t to = static_cast<int64_t>(t.r0 + c + j) * args.ldo + f;
           if constexpr (OUT == kTypeFp32)
             static_cast<float*>(args.out)[to] = sum * scale;
@@ -418,7 +435,8 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
   } else if (warp >= F4_FIRST_EPI) {
     // ------------------------------------------------------------ results
     const int quarter = warp & 3, part = (warp - F4_FIRST_EPI) >> 2;  // 64 columns of a lane quarter
-    const float scale = (args.alpha_a ? __ldcg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldcg(args.alpha_b) : 1.0f);
+    const TensorScales by = tensor_scales(args.alpha_a, args.alpha_b);
+    const float scale = by.scale;
     // two features of a row go as one 4-byte store where every row starts on 4 bytes
     const bool pairs =
         ((args.n | args.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(args.out) & 3) == 0;
@@ -437,6 +455,12 @@ __global__ void __launch_bounds__(F4_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_at(map_to_cta(&tail->acc_empty, first));
+      if (by.first != 1.0f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[h][j] = __float_as_uint(__uint_as_float(v[h][j]) * by.first);
+      }
       // a lane holds feature f of 32 consecutive rows, twice
       const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
 #pragma unroll

@@ -209,6 +209,38 @@ def test_product(bm, m, n, k, fmt, out):
     _close(y, va @ vb.t(), va.abs() @ vb.abs().t(), k)
 
 
+@pytest.mark.parametrize("alpha_a,alpha_b,scale,code", [
+    # the product of the scales underflows (to 0, or to a few bits) or overflows; the result does not
+    (1e-23, 1e-23, 0x7E, 0x7), (3e-42, 0.4, 0x7E, 0x7), (2e-20, 3e-24, 0x7E, 0x7), (2e-24, 1e-21, 0x7E, 0x7),
+    (-1e-23, 1e-23, 0x7E, 0x7), (2e38, 40.0, 0x01, 0x1), (30.0, 3e38, 0x01, 0x1), (1e20, -1e19, 0x01, 0x1),
+    # ordinary ones, a zero, and results that overflow or vanish for good
+    (0.37, 1.3, 0x38, 0x2), (0.0, 3e38, 0x7E, 0x7), (1e30, 1e30, 0x7E, 0x7), (1e-40, 1e-40, 0x7E, 0x7)])
+@pytest.mark.parametrize("out", [BF16, FP16, FP32])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 2592), (70, 130, 288), (33, 129, 96)])
+def test_tensor_scales_of_any_size(bm, m, n, k, out, alpha_a, alpha_b, scale, code):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(50)
+    codes = [torch.randint(0, 256, (r, k // 2), generator=g, device="cuda", dtype=torch.uint8) & 0x88 | 0x11 * code
+             for r in (m, n)]
+    for c in codes:
+        c[-1] = 0  # sums of zero stay zero
+    sf = [torch.full((r, (k // 16 + 15) // 16 * 16), scale, dtype=torch.uint8, device="cuda")[:, :k // 16]
+          for r in (m, n)]
+    al = [torch.tensor([v], dtype=FP32, device="cuda") for v in (alpha_a, alpha_b)]
+    y = bm.beam_moe_gemm_fp4(codes[0], sf[0], codes[1], sf[1], "nvfp4", alpha_a=al[0], alpha_b=al[1], out_dtype=out)
+    # the tensor scales multiply the reference's sums: those of codes and block scales are exact in 64
+    # bits (multiples of 2^-20 below 2^35), where with the scales in every term a sum that cancels to
+    # zero left a rounding of 1e-16 of terms of 1e66
+    va, vb, by = _values(codes[0], sf[0], "nvfp4"), _values(codes[1], sf[1], "nvfp4"), al[0].item() * al[1].item()
+    ref, size = (va @ vb.t()) * by, (va.abs() @ vb.abs().t()) * abs(by)
+    top = torch.finfo(out).max
+    over = ref.abs() > 2 * top  # (no reference lies between the type's largest value and twice that)
+    assert not bool(((ref.abs() > top) & ~over).any())
+    assert torch.equal(torch.isinf(y), over) and torch.equal(torch.sign(y)[over].double(), torch.sign(ref)[over])
+    y, ref, size = (torch.where(over, 0, t) for t in (y, ref, size))
+    _close(y, ref, size, k)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_product_strides_and_padding(bm, fmt):
     # operands that are column slices, an output inside a larger one, NaN bytes between the
