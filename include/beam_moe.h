@@ -343,8 +343,9 @@ BEAM_MOE_API beam_moe_status beam_moe_quantize_mxfp8(const float* src, int64_t r
  *   - x [rows][k], dy [rows][n] and w [groups][n][k] (contiguous) of `type` BEAM_MOE_BF16 or
  *     BEAM_MOE_FP16; y, dx and dw [groups][n][k] (contiguous) of out_type: `type` or
  *     BEAM_MOE_FP32.  ld* are the elements from one row to the next: at least the row's
- *     length, a multiple of 8.  Tensors start on 16-byte boundaries and do not overlap the
- *     output.
+ *     length, a multiple of 8.  Tensors start on 16-byte boundaries.  An output that shares
+ *     memory with an operand is INVALID_ARG (columns of one larger matrix do not, nor do an output
+ *     and the gaps between an operand's rows).
  *   - n and k are multiples of 8, 1 <= groups <= 1024, rows < 2^31 - 2^16 (else UNSUPPORTED).
  *     An expert may have no rows: its dw is zero.  rows == 0 enqueues nothing (wgrad: zeroes).
  *   - offsets are only read on the device: they may come from the kernel before, and a
@@ -380,7 +381,8 @@ BEAM_MOE_API beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t
  * [rows][cols / 32 or cols / 16], both row-major; their rows may be further apart (ldc, ldsf:
  * bytes from one row to the next, multiples of 16).  What lies between a row's last scale and
  * the next row is neither written nor used.  cols is a multiple of 32 (else UNSUPPORTED); all
- * pointers start on 16-byte boundaries, tensor scales on 4-byte ones. */
+ * pointers start on 16-byte boundaries, tensor scales on 4-byte ones.  An output that shares memory
+ * with an operand or with another output is INVALID_ARG. */
 enum { BEAM_MOE_FP4_MX = 0, BEAM_MOE_FP4_NV = 1 };
 
 /* src [rows][cols] of src_type (BF16, FP16 or FP32), rows ld elements apart (a multiple of 16

@@ -42,6 +42,7 @@
 #include "../../include/beam_moe.h"
 #include "cta_pair.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace beam {
 
@@ -593,6 +594,11 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
       lda_sf % 16 != 0 || ldb_sf % 16 != 0 || ldo < n)
     return BEAM_MOE_ERR_INVALID_ARG;
   const bool mx = format == BEAM_MOE_FP4_MX;
+  const int64_t size = out_type == BEAM_MOE_FP32 ? 4 : 2;
+  if (overlaps_any({out, m, n * size, ldo * size},
+                   {{a_codes, m, k / 2, lda}, {a_sf, m, scales, lda_sf}, {b_codes, n, k / 2, ldb},
+                    {b_sf, n, scales, ldb_sf}, {mx ? nullptr : alpha_a, 1, 4, 4}, {mx ? nullptr : alpha_b, 1, 4, 4}}))
+    return BEAM_MOE_ERR_INVALID_ARG;
   const int blocks = (m + F4_TILE - 1) / F4_TILE;
   const int height = ((m + blocks - 1) / blocks + 31) / 32 * 32;
   Fp4Maps maps;

@@ -50,6 +50,7 @@
 #include "../../include/beam_moe.h"
 #include "cta_pair.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace beam {
 
@@ -578,6 +579,16 @@ beam_moe_status check_grouped(int32_t rows, int32_t groups, int32_t n, int32_t k
 // A [rows][cols] operand whose rows are ld elements apart.
 bool good_rows(const void* p, int64_t ld, int32_t cols) { return p && aligned16(p) && ld >= cols && ld % 8 == 0; }
 
+Span rows_span(const void* p, int32_t rows, int32_t cols, int64_t ld, int32_t type) {
+  const int64_t size = type == BEAM_MOE_FP32 ? 4 : 2;
+  return {p, rows, cols * size, ld * size};
+}
+Span weights_span(const void* p, int32_t groups, int32_t n, int32_t k, int32_t type) {
+  const int64_t row = static_cast<int64_t>(k) * (type == BEAM_MOE_FP32 ? 4 : 2);
+  return {p, static_cast<int64_t>(groups) * n, row, row};
+}
+Span offsets_span(const int32_t* p, int32_t groups) { return {p, groups + 1, 4, 4}; }
+
 beam_moe_status launch_status(cudaError_t e) {
   return e == cudaSuccess ? BEAM_MOE_OK : e == cudaErrorNotSupported ? BEAM_MOE_ERR_UNSUPPORTED : BEAM_MOE_ERR_CUDA;
 }
@@ -593,8 +604,11 @@ beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w,
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kFwd, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || y == x || y == w || !offsets ||
+  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (overlaps_any(rows_span(y, rows, n, ldy, out_type),
+                   {rows_span(x, rows, k, ldx, type), weights_span(w, groups, n, k, type), offsets_span(offsets, groups)}))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kFwd, x, ldx, nullptr, 0, w, offsets, rows, groups, n, k, type, y, ldy,
                                            out_type, static_cast<cudaStream_t>(stream)));
@@ -607,8 +621,11 @@ beam_moe_status beam_moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const 
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kDgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || dx == dy || dx == w || !offsets ||
+  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || !offsets ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (overlaps_any(rows_span(dx, rows, k, lddx, out_type),
+                   {rows_span(dy, rows, n, lddy, type), weights_span(w, groups, n, k, type), offsets_span(offsets, groups)}))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kDgrad, dy, lddy, nullptr, 0, w, offsets, rows, groups, n, k, type, dx,
                                            lddx, out_type, static_cast<cudaStream_t>(stream)));
@@ -625,8 +642,10 @@ beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const 
   if (rows == 0)  // no rows: every gradient is zero
     return launch_status(cudaMemsetAsync(
         dw, 0, static_cast<size_t>(groups) * n * static_cast<size_t>(k) * (out_type == BEAM_MOE_FP32 ? 4 : 2), s));
-  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || dw == dy || dw == x || !offsets ||
-      (reinterpret_cast<uintptr_t>(offsets) & 3))
+  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 3))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (overlaps_any(weights_span(dw, groups, n, k, out_type),
+                   {rows_span(dy, rows, n, lddy, type), rows_span(x, rows, k, ldx, type), offsets_span(offsets, groups)}))
     return BEAM_MOE_ERR_INVALID_ARG;
   return launch_status(launch_grouped_gemm(kWgrad, x, ldx, dy, lddy, nullptr, offsets, rows, groups, n, k, type, dw, k,
                                            out_type, s));

@@ -21,6 +21,7 @@
 #include "../../include/beam_moe.h"
 #include "common.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace beam {
 
@@ -450,6 +451,11 @@ beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t s
   const bool given = alpha > 0.0f && alpha <= 3.4028235e38f;
   if (nv && !given && (!(alpha <= 0.0f) || !alpha_out)) return BEAM_MOE_ERR_INVALID_ARG;  // infinite, NaN
   if (nv && alpha_out && !aligned_to(alpha_out, 4)) return BEAM_MOE_ERR_INVALID_ARG;
+  const Span in{src, rows, static_cast<int64_t>(cols) * size, ld * size}, out_codes{codes, rows, cols / 2, ldc},
+      out_sf{sf, rows, scale_bytes(format, cols), ldsf}, out_alpha{nv ? alpha_out : nullptr, 1, 4, 4};
+  if (overlaps_any(in, {out_codes, out_sf, out_alpha}) || overlaps_any(out_codes, {out_sf, out_alpha}) ||
+      overlap(out_sf, out_alpha))
+    return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const float* amax = nullptr;
   if (nv && !given) {
@@ -480,6 +486,10 @@ beam_moe_status beam_moe_dequantize_fp4(int32_t format, const uint8_t* codes, in
   if (!codes || !sf || !out || !aligned_to(codes, 16) || !aligned_to(out, 16) || (alpha && !aligned_to(alpha, 4)))
     return BEAM_MOE_ERR_INVALID_ARG;
   if (ldo < cols || ldo * size % 16 != 0 || ldc < cols / 2 || ldc % 16 != 0 || ldsf < scale_bytes(format, cols))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (overlaps_any({out, rows, static_cast<int64_t>(cols) * size, ldo * size},
+                   {{codes, rows, cols / 2, ldc}, {sf, rows, scale_bytes(format, cols), ldsf},
+                    {format == BEAM_MOE_FP4_NV ? alpha : nullptr, 1, 4, 4}}))
     return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto run = format == BEAM_MOE_FP4_MX ? launch_dequantize<BEAM_MOE_FP4_MX> : launch_dequantize<BEAM_MOE_FP4_NV>;

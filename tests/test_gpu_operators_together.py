@@ -150,3 +150,31 @@ def test_routing_right_behind_the_operators(bm, tokens, hidden, experts):
     torch.cuda.synchronize()
     got = [step(v, False) for v in inputs]
     assert all(torch.equal(a, b) for g, r in zip(got, want) for a, b in zip(g, r))
+
+
+def test_columns_of_one_buffer(bm):
+    # operands and outputs that are columns of the same matrix do not share memory, and are taken
+    rows, n, k = 70, 40, 96
+    buf = _draw((rows, 256), BF16, 70)
+    w, off = _draw((2, n, k), BF16, 71, 0.1), torch.tensor([0, 30, rows], dtype=torch.int32, device="cuda")
+    want = bm.beam_moe_grouped_gemm(buf[:, :k].contiguous(), w, off)
+    got = bm.beam_moe_grouped_gemm(buf[:, :k], w, off, out=buf[:, k:k + n])
+    assert torch.equal(got, want) and got.data_ptr() == buf[:, k:].data_ptr()
+    dwant = bm.beam_moe_grouped_gemm_dgrad(want, w, off)
+    assert torch.equal(bm.beam_moe_grouped_gemm_dgrad(buf[:, k:k + n], w, off, out=buf[:, 144:144 + k]), dwant)
+    with pytest.raises(bm.BeamMoeError) as err:
+        bm.beam_moe_grouped_gemm(buf[:, :k], w, off, out=buf[:, k - 8:k - 8 + n])
+    assert err.value.status == bm.ERR_INVALID_ARG
+    # codes and scales of one buffer's rows; the product's result behind them
+    for fmt, block in (("mxfp4", 32), ("nvfp4", 16)):
+        q = bm.beam_moe_quantize_fp4(dwant, fmt)
+        whole = torch.zeros((rows, 256), dtype=torch.uint8, device="cuda")
+        codes, sf = whole[:, :k // 2], whole[:, 48:48 + k // block]
+        codes.copy_(q[0])
+        sf.copy_(q[1])
+        out = torch.as_strided(whole.view(BF16), (rows, 60), (128, 1), 32)
+        other = [t[:60] for t in q[:2]]
+        ref = bm.beam_moe_gemm_fp4(q[0], q[1], other[0], other[1], fmt, alpha_a=q[2], alpha_b=q[2])
+        assert torch.equal(bm.beam_moe_gemm_fp4(codes, sf, other[0], other[1], fmt, alpha_a=q[2], alpha_b=q[2],
+                                                out=out), ref)
+        assert torch.equal(codes, q[0]) and torch.equal(sf, q[1])

@@ -104,7 +104,7 @@ def test_fp4_quantiser():
     assert _quantize(form=bm.FP4_NV, alpha=0.0) == BAD             # nowhere to put the scale found
     assert _quantize(form=bm.FP4_NV, alpha=float("inf")) == BAD
     assert _quantize(form=bm.FP4_NV, alpha_out=P + 2) == BAD
-    assert _quantize(form=bm.FP4_NV, alpha=float("nan"), alpha_out=P) == BAD  # not "find the scale"
+    assert _quantize(form=bm.FP4_NV, alpha=float("nan"), codes=2 * P, sf=3 * P, alpha_out=4 * P) == BAD
 
 
 def test_fp4_product():
