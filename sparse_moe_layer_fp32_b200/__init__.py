@@ -534,8 +534,11 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     codes = _empty(src, (rows, cols // 2), torch.uint8, stream)
     sf = _empty(src, (rows, pitch), torch.uint8, stream)
     scale = None
-    if fmt == "nvfp4":  # the library writes it; an empty tensor has none
-        scale = _empty(src, (1,), torch.float32, stream) if rows and cols else src.new_zeros(1, dtype=torch.float32)
+    if fmt == "nvfp4":
+        scale = _empty(src, (1,), torch.float32, stream)
+        if not (rows and cols):  # the library, which writes it, has nothing to do
+            with torch.cuda.stream(stream):
+                scale.fill_(0.0 if alpha is None else alpha)
     _call("beam_moe_quantize_fp4", index, stream, form, src.data_ptr(), kind, ld, rows, cols,
           -1.0 if alpha is None else alpha, codes.data_ptr(), cols // 2, sf.data_ptr(), pitch,
           None if scale is None else scale.data_ptr())

@@ -327,6 +327,16 @@ def test_nothing_to_do(bm):
         assert bm.beam_moe_gemm_fp4(q[0], q[1], codes, sf, fmt).shape == (5, 0)
 
 
+def test_tensor_scale_of_an_empty_matrix(bm):
+    # the scale that was given, else 0; written on the call's stream
+    none, side = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.cuda.Stream()
+    assert bm.beam_moe_quantize_fp4(none, "nvfp4", alpha=0.002)[2].item() == np.float32(0.002)
+    assert bm.beam_moe_quantize_fp4(none, "nvfp4")[2].item() == 0
+    scale = bm.beam_moe_quantize_fp4(none, "nvfp4", alpha=0.002, stream=side)[2]
+    side.synchronize()
+    assert scale.item() == np.float32(0.002)
+
+
 def test_streams_and_a_replayed_graph(bm):
     m, n, k = 70, 300, 544
     x, w = _draw((m, k), BF16, 29), _draw((n, k), BF16, 30)
