@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -347,6 +348,10 @@ def beam_moe_profile_read(h):
 # ------------------------------------------------------------------ operators on tensors
 # The smallest of these calls take a few microseconds on the GPU, so the checks below avoid
 # building objects: plain integers go to ctypes, and a stream is looked up by its number.
+#
+# `stream` (None: the current one) is where a call runs and where what it allocates belongs.  Inputs
+# from another stream stay the caller's: ordered before the call, and kept (or recorded on `stream`)
+# until it has read them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -393,7 +398,14 @@ def _row_stride(t, what):
     return step if rows > 1 else cols  # a single row's pitch is never stepped over
 
 
+def _warn_no_gradient(level, a, b=None):
+    if torch.is_grad_enabled() and (a.requires_grad or (b is not None and b.requires_grad)):
+        warnings.warn("the result carries no gradient for its inputs: those of the grouped products are "
+                      "beam_moe_grouped_gemm_dgrad and beam_moe_grouped_gemm_wgrad", stacklevel=level)
+
+
 def _grouped(offsets, a, b):
+    _warn_no_gradient(4, a, b)
     kind = a.dtype
     if (kind is not torch.bfloat16 and kind is not torch.float16) or b.dtype is not kind:
         raise ValueError("the operands have to be both BF16 or both FP16")
@@ -429,7 +441,8 @@ def beam_moe_grouped_gemm(x, w, offsets, out=None, out_dtype=None, stream=None):
 
     x [rows, k] and w [groups, n, k] BF16 or FP16, offsets int32 [groups + 1], all on one device;
     y [rows, n] in x's type or FP32 (out's, else out_dtype, else x's).  Rows of no expert are not
-    written."""
+    written.  y carries no gradient (a warning says so where an input requires one):
+    beam_moe_grouped_gemm_dgrad and beam_moe_grouped_gemm_wgrad compute them."""
     kind = _grouped(offsets, x, w)
     groups, n, k = _expert_weights(w, offsets)
     ldx = _row_stride(x, "x")
@@ -519,6 +532,7 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     alpha is the tensor scale, a float; None takes the largest finite value / 2688, found on
     the device.  The alpha returned is an FP32 tensor [1] (None for MXFP4)."""
     form = _fp4_format(fmt)
+    _warn_no_gradient(3, src)
     kind = TYPES.get(src.dtype)
     if kind is None:
         raise ValueError("src has to be BF16, FP16 or FP32")

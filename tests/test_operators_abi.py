@@ -1,5 +1,7 @@
 """The operators on caller buffers answer bad arguments on the host, before any CUDA call."""
 
+import warnings
+
 import pytest
 import torch
 
@@ -162,3 +164,25 @@ def test_tensor_scales_that_single_precision_does_not_hold():
     for alpha in (8e-46, 1e-45, 3.4e38):  # the smallest and the largest pass to the next check
         with pytest.raises(ValueError, match="device"):
             bm.beam_moe_quantize_fp4(x, "nvfp4", alpha=alpha)
+
+
+def test_an_input_that_requires_a_gradient_is_warned_about():
+    # the results carry no gradient (every call ends at the check of the device)
+    x, w = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(2, 16, 32, dtype=torch.bfloat16)
+    dy, off = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    xg, wg = x.clone().requires_grad_(), w.clone().requires_grad_()
+    calls = [(lambda x, w: bm.beam_moe_grouped_gemm(x, w, off), (x, w), (xg, w), (x, wg)),
+             (lambda w: bm.beam_moe_grouped_gemm_dgrad(dy, w, off), (w,), (wg,)),
+             (lambda x: bm.beam_moe_grouped_gemm_wgrad(dy, x, off), (x,), (xg,)),
+             (lambda x: bm.beam_moe_quantize_fp4(x, "mxfp4"), (x,), (xg,))]
+    for call, plain, *traced in calls:
+        for args in traced:
+            with pytest.warns(UserWarning, match="gradient") as seen, pytest.raises(ValueError, match="device"):
+                call(*args)
+            assert seen[0].filename == __file__  # the caller's line
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with pytest.raises(ValueError, match="device"):
+                call(*plain)
+            with torch.no_grad(), pytest.raises(ValueError, match="device"):
+                call(*traced[0])
