@@ -1,6 +1,8 @@
 """The operators in a row, as a program uses them: a BF16 mixture-of-experts layer trained through
 the routing and the grouped products, and 4-bit projections one after another."""
 
+import os
+
 import pytest
 import torch
 
@@ -178,3 +180,24 @@ def test_columns_of_one_buffer(bm):
         assert torch.equal(bm.beam_moe_gemm_fp4(codes, sf, other[0], other[1], fmt, alpha_a=q[2], alpha_b=q[2],
                                                 out=out), ref)
         assert torch.equal(codes, q[0]) and torch.equal(sf, q[1])
+
+
+def test_the_readme_example(bm, repo_root):
+    with open(os.path.join(repo_root, "README.md")) as f:
+        code = [part for part in f.read().split("```") if part.startswith("python") and "grouped_gemm(" in part]
+    assert len(code) == 1
+    tokens, hidden, inter, experts, top_k = 40, 256, 128, 16, 2
+    names = dict(bm=bm, torch=torch, E=experts, top_k=top_k, x=_draw((tokens, hidden), BF16, 80),
+                 router_w=_draw((experts, hidden), FP32, 81), proj=_draw((96, hidden), FP32, 82, 0.05),
+                 w_gate_up=_draw((experts, 2 * inter, hidden), BF16, 83, 0.06),
+                 dy=_draw((tokens * top_k, 2 * inter), BF16, 84))
+    exec(code[0].removeprefix("python"), names)
+    assert names["y"].shape == (tokens * top_k, 2 * inter) and names["dx"].shape == (tokens * top_k, hidden)
+    assert names["dw"].shape == (experts, 2 * inter, hidden) and names["out"].shape == (tokens, 96)
+    for slot in range(tokens * top_k):
+        e = int(names["ids"].flatten()[names["order"][slot]])
+        row = names["x"][int(names["order"][slot]) // top_k].double()
+        ref = names["w_gate_up"][e].double() @ row
+        size = names["w_gate_up"][e].double().abs() @ row.abs()
+        # 16 additions into FP32 of at most 2^-22 of the absolute sum, one rounding to BF16
+        assert bool(((names["y"][slot].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -17 * size).all())
