@@ -337,3 +337,19 @@ def test_refusals(bm):
         with pytest.raises(bm.BeamMoeError) as err:
             call()
         assert err.value.status == status
+
+
+@pytest.mark.parametrize("counts,n,k", SHAPES)
+def test_fp16_gradients_in_fp32(bm, counts, n, k):
+    rows = sum(counts)
+    dy, x, w = _draw((rows, n), FP16, 60), _draw((rows, k), FP16, 61), _draw((len(counts), n, k), FP16, 62, 0.1)
+    dx = bm.beam_moe_grouped_gemm_dgrad(dy, w, _offsets(counts), out_dtype=FP32)
+    dw = bm.beam_moe_grouped_gemm_wgrad(dy, x, _offsets(counts), out_dtype=FP32)
+    assert dx.dtype == dw.dtype == FP32
+    for r, ref, size in _fwd_ref(dy, w.transpose(1, 2), counts):
+        _close(dx[r], ref, size, n)
+    a = 0
+    for e, c in enumerate(counts):
+        d, v = dy[a:a + c].double(), x[a:a + c].double()
+        _close(dw[e], d.t() @ v, d.abs().t() @ v.abs(), max(c, 1), e)
+        a += c
