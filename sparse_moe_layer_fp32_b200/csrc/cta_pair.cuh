@@ -251,20 +251,19 @@ __device__ __forceinline__ uint32_t trade_pair(uint32_t lo, uint32_t hi, float s
 
 // Accumulators whose lanes are features and whose columns are rows of the output, stored in rows:
 // four warps (one per lane quarter) hold 32 columns of this CTA's 128 features; v: this lane's
-// feature in rows row0 .. row0 + 31.  The 32 x 128 values are turned in 8 KB of shared memory and leave as whole
-// 256-byte rows (against 64-byte pieces straight from the lanes: 1% less time for the grouped
-// products; the 4-bit product is 3 to 9% faster without).  out: 16-byte aligned rows; f0: the CTA's first feature, features a multiple of 8;
-// barrier: a named barrier of these four warps.
+// feature in rows row0 .. row0 + 31.  The 32 x 128 values are turned in 8 KB of shared memory and
+// leave as whole 256-byte rows (against 64-byte pieces straight from the lanes: 1% less time for the
+// grouped products; the 4-bit product is 3 to 9% faster without).  out: 16-byte aligned rows; f0: the
+// CTA's first feature, features a multiple of 8; barrier: a named barrier of these four warps.
 template <int OUT>
-__device__ __forceinline__ void store_turned(const uint32_t (&v)[32], float scale, uint8_t* turn, int barrier, int quarter,
-                                             int lane, uint16_t* out, int64_t ldo, int row0, int row_end, int f0,
-                                             int features) {
+__device__ __forceinline__ void store_turned(const uint32_t (&v)[32], uint8_t* turn, int barrier, int quarter, int lane,
+                                             uint16_t* out, int64_t ldo, int row0, int row_end, int f0, int features) {
   asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");  // the stretch before has left
   const int odd = lane & 1;
   uint8_t* to = turn + odd * 256 + ((quarter * 64 + (lane - odd) * 2) ^ (odd << 6));
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    *reinterpret_cast<uint32_t*>(to + j * 256) = trade_pair<OUT>(v[j], v[j + 1], scale, odd);
+    *reinterpret_cast<uint32_t*>(to + j * 256) = trade_pair<OUT>(v[j], v[j + 1], 1.0f, odd);
   }
   asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
   const int part = lane & 15, f = f0 + part * 8;

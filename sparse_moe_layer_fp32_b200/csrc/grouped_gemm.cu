@@ -33,10 +33,12 @@
 //
 // What bounds it.  A stage of an n-row tile is 2 n cycles of MMAs against about 256 + n for its
 // operands on their way through L2 and shared memory: they meet at 256 rows, where the tensor pipe
-// is active 89% of the cycles and the power limit sets the clock (16384 x 5120 x 5120 BF16 in
-// one group: 556 us, 1540 TFLOP/s, cuBLAS 550; 32 experts of 512 rows each, 5120 x 5120: 626 us).
-// Uneven experts lose to tiles of fewer rows (702 us).  With a row or a few for each expert it
-// streams weights: 64 rows over 256 experts of 1536 x 5120 in 151 us, 5.9 TB/s.
+// is active 89% of the cycles and the power limit sets the clock.  16384 x 5120 x 5120 BF16, from idle
+// and in a loop of a second: one group 578 and 670 us (cuBLAS 563 and 644), 32 experts of 512 rows
+// each 652 and 777; uneven experts lose to tiles of fewer rows (713 and 846).  With a row or a few for
+// each expert it streams weights: 64 rows over 256 experts of 1536 x 5120 in 146 to 154 us, 5.8 to
+// 6.1 TB/s.  A tile's sum is never divided: a product of few tiles leaves most pairs idle (gradient of
+// 4 experts of 256 x 256 over 32768 rows: 41 us on 4 of 74 pairs).
 //
 // The work list comes from the offsets, which only the device knows: every CTA scans them at
 // its start (at most 1024 experts).  They are read as their running maximum, clamped to
@@ -375,9 +377,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
           *reinterpret_cast<uint4*>(base + c * GG_CHUNK + (rows + r) * 128 + p * 16) = make_uint4(0, 0, 0, 0);
         }
         // The zeros are in this SM's shared memory, for the tensor core that reads it there, once
-        // the proxy fence has passed: the arrival that follows needs to carry nothing else.  (A
-        // release at cluster scope here waited for the storing warps' results as well: 496 against
-        // 433 us for 32768 rows of 64 experts, 1536 x 5120.)
+        // the proxy fence has passed: the arrival that follows needs to carry nothing else.  (With a
+        // release at cluster scope, in turn: 46.4 against 44.1 us for 3001 rows of 48 experts, 520 x
+        // 1000, FP16; no difference for 512 rows an expert.)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(map_to_cta(&tail->full[last], 0));
@@ -457,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GG_THREADS, 1)
             for (int j = 0; j < 32; ++j)
               if (ok && row + j < t.n_end && m < args.m) p[j * args.ldo] = __uint_as_float(v[j]);
           } else {
-            store_turned<OUT>(v, 1.0f, tail->turn + side * 8192, 1 + side, quarter, lane,
+            store_turned<OUT>(v, tail->turn + side * 8192, 1 + side, quarter, lane,
                               static_cast<uint16_t*>(args.out), args.ldo, row, ok ? t.n_end : row,
                               t.m0 + static_cast<int>(rank) * 128, args.m);
           }
