@@ -424,6 +424,8 @@ def _empty(like, shape, dtype, stream):
 
 def _output(out, like, shape, dtype, stream):
     if out is None:
+        if dtype not in TYPES:
+            raise ValueError("out_dtype has to be BF16, FP16 or FP32")
         return _empty(like, shape, dtype, stream)
     if out.shape != shape or out.dtype not in TYPES:
         raise ValueError(f"out has to be a BF16, FP16 or FP32 tensor of shape {shape}")
@@ -519,7 +521,7 @@ def _fp4_matrix(codes, sf, fmt, what):
 def _tensor_scale(alpha, fmt, what):
     if alpha is None or fmt == "mxfp4":
         return None
-    if alpha.dtype is not torch.float32 or alpha.numel() != 1:
+    if getattr(alpha, "dtype", None) is not torch.float32 or alpha.numel() != 1:
         raise ValueError(f"{what} has to be one FP32 value on the device")
     return alpha
 

@@ -186,3 +186,22 @@ def test_an_input_that_requires_a_gradient_is_warned_about():
                 call(*plain)
             with torch.no_grad(), pytest.raises(ValueError, match="device"):
                 call(*traced[0])
+
+
+def test_types_that_are_none_of_the_operators():
+    x, w = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(2, 16, 32, dtype=torch.bfloat16)
+    dy, off = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    codes, sf = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 16, dtype=torch.uint8)[:, :4]
+    for kind in (torch.float64, torch.int32, torch.float8_e4m3fn):
+        for call in (lambda: bm.beam_moe_grouped_gemm(x, w, off, out_dtype=kind),
+                     lambda: bm.beam_moe_grouped_gemm_dgrad(dy, w, off, out_dtype=kind),
+                     lambda: bm.beam_moe_grouped_gemm_wgrad(dy, x, off, out_dtype=kind),
+                     lambda: bm.beam_moe_gemm_fp4(codes, sf, codes, sf, "nvfp4", out_dtype=kind),
+                     lambda: bm.beam_moe_dequantize_fp4(codes, sf, "nvfp4", out_dtype=kind)):
+            with pytest.raises(ValueError, match="BF16, FP16 or FP32"):
+                call()
+    for alpha in (0.5, torch.ones(1, dtype=torch.float64), torch.ones(2)):  # one FP32 value on the device
+        with pytest.raises(ValueError, match="alpha"):
+            bm.beam_moe_gemm_fp4(codes, sf, codes, sf, "nvfp4", alpha_a=alpha)
+        with pytest.raises(ValueError, match="alpha"):
+            bm.beam_moe_dequantize_fp4(codes, sf, "nvfp4", alpha=alpha)
