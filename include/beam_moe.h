@@ -387,10 +387,10 @@ enum { BEAM_MOE_FP4_MX = 0, BEAM_MOE_FP4_NV = 1 };
 
 /* src [rows][cols] of src_type (BF16, FP16 or FP32), rows ld elements apart (a multiple of 16
  * bytes).  alpha and alpha_out as in beam_moe_quantize_nvfp4: alpha > 0 is NVFP4's tensor scale
- * (infinity and NaN are INVALID_ARG); alpha <= 0 takes the largest finite |src| / 2688, found on the device.  alpha_out (device
- * FP32; may be NULL where alpha > 0) receives the scale used.  MXFP4 uses neither.  A block that
- * holds a NaN or an infinity gets a NaN scale and zero codes: it reads back, and multiplies, as
- * NaN. */
+ * (infinity and NaN are INVALID_ARG); alpha <= 0 takes the largest finite |src| / 2688, found on the
+ * device.  alpha_out (device FP32; may be NULL where alpha > 0) receives the scale used.  MXFP4 uses
+ * neither.  A block that holds a NaN or an infinity gets a NaN scale and zero codes: it reads back,
+ * and multiplies, as NaN.  No rows or no columns: nothing is enqueued and alpha_out is not written. */
 BEAM_MOE_API beam_moe_status beam_moe_quantize_fp4(int32_t format, const void* src, int32_t src_type, int64_t ld,
                                                    int64_t rows, int32_t cols, float alpha, uint8_t* codes,
                                                    int64_t ldc, uint8_t* sf, int64_t ldsf, float* alpha_out,
@@ -419,10 +419,12 @@ BEAM_MOE_API beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_
  * gave up since the last check, and the outputs of the call that it belongs to are not complete. */
 BEAM_MOE_API beam_moe_status beam_moe_check_operators(void* stream);
 /* Test support: runs the operators' bounded wait, with a limit of limit_ns (up to 0.5 s), into its
- * limit on `stream`.  result (device int32 [4]): [0] 1 where the wait gave up and told its CTA; two CTAs hand sums over as in a tile that several pairs share: [1] 1 where a sender that gave up
+ * limit on `stream`.  result (device int32 [4]): [0] 1 where the wait gave up and told its CTA; two
+ * CTAs hand sums over as in a tile that several pairs share: [1] 1 where a sender that gave up
  * released the receiver, [2] 1 where a receiver that gave up stayed until a late sender's sums had
  * landed; [3] 1 where a wait of three limits was met because the role before it made progress, and
- * one without progress was not.  The error words are set as by the operators, so that the next check returns TIMEOUT. */
+ * one without progress was not.  The error words are set as by the operators, so that the next
+ * check returns TIMEOUT. */
 BEAM_MOE_API beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* result, void* stream);
 
 /* Internal buffers of the last forward, for tests (layouts in the comment of each id). */
