@@ -562,7 +562,7 @@ cudaError_t launch_format(int out_type, const Fp4Args& a, const Fp4Maps& maps, c
   return launch_fp4<FORMAT, kTypeFp32>(a, maps, s);
 }
 
-bool on(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool on(const void* p, uintptr_t a) { return p && aligned_to(p, a); }
 
 }  // namespace
 
@@ -612,5 +612,5 @@ extern "C" beam_moe_status beam_moe_gemm_fp4(int32_t format, const uint8_t* a_co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mx ? launch_format<BEAM_MOE_FP4_MX>(out_type, args, maps, s)
                            : launch_format<BEAM_MOE_FP4_NV>(out_type, args, maps, s);
-  return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA;
+  return launch_status(e);
 }

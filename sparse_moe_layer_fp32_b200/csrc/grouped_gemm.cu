@@ -565,8 +565,6 @@ using namespace beam;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // The checks that the three products share.
 beam_moe_status check_grouped(int32_t rows, int32_t groups, int32_t n, int32_t k, int32_t type, int32_t out_type) {
   if (rows < 0 || groups < 1 || n < 1 || k < 1) return BEAM_MOE_ERR_INVALID_ARG;
@@ -579,7 +577,7 @@ beam_moe_status check_grouped(int32_t rows, int32_t groups, int32_t n, int32_t k
 }
 
 // A [rows][cols] operand whose rows are ld elements apart.
-bool good_rows(const void* p, int64_t ld, int32_t cols) { return p && aligned16(p) && ld >= cols && ld % 8 == 0; }
+bool good_rows(const void* p, int64_t ld, int32_t cols) { return p && aligned_to(p, 16) && ld >= cols && ld % 8 == 0; }
 
 Span rows_span(const void* p, int32_t rows, int32_t cols, int64_t ld, int32_t type) {
   const int64_t size = type == BEAM_MOE_FP32 ? 4 : 2;
@@ -590,10 +588,6 @@ Span weights_span(const void* p, int32_t groups, int32_t n, int32_t k, int32_t t
   return {p, static_cast<int64_t>(groups) * n, row, row};
 }
 Span offsets_span(const int32_t* p, int32_t groups) { return {p, groups + 1, 4, 4}; }
-
-beam_moe_status launch_status(cudaError_t e) {
-  return e == cudaSuccess ? BEAM_MOE_OK : e == cudaErrorNotSupported ? BEAM_MOE_ERR_UNSUPPORTED : BEAM_MOE_ERR_CUDA;
-}
 
 }  // namespace
 
@@ -606,8 +600,8 @@ beam_moe_status beam_moe_grouped_gemm(const void* x, int64_t ldx, const void* w,
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kFwd, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned16(w) || !offsets ||
-      (reinterpret_cast<uintptr_t>(offsets) & 3))
+  if (!good_rows(x, ldx, k) || !good_rows(y, ldy, n) || !w || !aligned_to(w, 16) || !offsets ||
+      !aligned_to(offsets, 4))
     return BEAM_MOE_ERR_INVALID_ARG;
   if (overlaps_any(rows_span(y, rows, n, ldy, out_type),
                    {rows_span(x, rows, k, ldx, type), weights_span(w, groups, n, k, type), offsets_span(offsets, groups)}))
@@ -623,8 +617,8 @@ beam_moe_status beam_moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const 
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kDgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
   if (rows == 0) return BEAM_MOE_OK;
-  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned16(w) || !offsets ||
-      (reinterpret_cast<uintptr_t>(offsets) & 3))
+  if (!good_rows(dy, lddy, n) || !good_rows(dx, lddx, k) || !w || !aligned_to(w, 16) || !offsets ||
+      !aligned_to(offsets, 4))
     return BEAM_MOE_ERR_INVALID_ARG;
   if (overlaps_any(rows_span(dx, rows, k, lddx, out_type),
                    {rows_span(dy, rows, n, lddy, type), weights_span(w, groups, n, k, type), offsets_span(offsets, groups)}))
@@ -639,12 +633,12 @@ beam_moe_status beam_moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const 
   const beam_moe_status st = check_grouped(rows, groups, n, k, type, out_type);
   if (st != BEAM_MOE_OK) return st;
   if (grouped_gemm_most_tiles(kWgrad, rows, groups, n, k) > (1 << 30)) return BEAM_MOE_ERR_UNSUPPORTED;
-  if (!dw || !aligned16(dw)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (!dw || !aligned_to(dw, 16)) return BEAM_MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0)  // no rows: every gradient is zero
     return launch_status(cudaMemsetAsync(
         dw, 0, static_cast<size_t>(groups) * n * static_cast<size_t>(k) * (out_type == BEAM_MOE_FP32 ? 4 : 2), s));
-  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 3))
+  if (!good_rows(dy, lddy, n) || !good_rows(x, ldx, k) || !offsets || !aligned_to(offsets, 4))
     return BEAM_MOE_ERR_INVALID_ARG;
   if (overlaps_any(weights_span(dw, groups, n, k, out_type),
                    {rows_span(dy, rows, n, lddy, type), rows_span(x, rows, k, ldx, type), offsets_span(offsets, groups)}))

@@ -251,6 +251,10 @@ cudaError_t launch_finalize(const uint16_t* y, const float* w, const int32_t* in
 constexpr int kTypeBf16 = BEAM_MOE_BF16, kTypeFp16 = BEAM_MOE_FP16, kTypeFp32 = BEAM_MOE_FP32;
 // cuTensorMapEncodeTiled, or nullptr where the driver has none (beam_moe.cu).
 void* tensor_map_encode_fn();
+inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline beam_moe_status launch_status(cudaError_t e) {
+  return e == cudaSuccess ? BEAM_MOE_OK : e == cudaErrorNotSupported ? BEAM_MOE_ERR_UNSUPPORTED : BEAM_MOE_ERR_CUDA;
+}
 // Address of the current device's error word of these kernels.
 cudaError_t grouped_gemm_error_word(uint32_t** word);
 cudaError_t gemm_fp4_error_word(uint32_t** word);

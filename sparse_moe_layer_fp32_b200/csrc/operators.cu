@@ -127,7 +127,7 @@ beam_moe_status beam_moe_check_operators(void* stream) {
 
 beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* result, void* stream) {
   if (limit_ns <= 0 || limit_ns > static_cast<int64_t>(kWaitLimitNs / 4) || !result ||
-      (reinterpret_cast<uintptr_t>(result) & 3))
+      !aligned_to(result, 4))
     return BEAM_MOE_ERR_INVALID_ARG;
   uint32_t *grouped = nullptr, *fp4 = nullptr;
   cudaError_t e = grouped_gemm_error_word(&grouped);
@@ -139,7 +139,7 @@ beam_moe_status beam_moe_debug_operators_timeout(int64_t limit_ns, int32_t* resu
   for (int late = 0; late < 2 && e == cudaSuccess; ++late)
     e = launch_pdl_clusters(sums_probe_kernel, 2, 2, 32, 0, static_cast<cudaStream_t>(stream),
                             static_cast<uint64_t>(limit_ns), late, result + 1 + late);
-  return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA;
+  return launch_status(e);
 }
 
 }  // extern "C"

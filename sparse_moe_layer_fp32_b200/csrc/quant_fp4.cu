@@ -369,9 +369,6 @@ cudaError_t for_shares(int64_t rows, int64_t cols, int values, bool flat, F f) {
   return cudaSuccess;
 }
 
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-beam_moe_status launch_status(cudaError_t e) { return e == cudaSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_CUDA; }
-
 template <int TYPE>
 cudaError_t launch_quantize(int format, const void* src, int64_t ld, int64_t rows, int cols, float alpha,
                             const float* amax_dev, uint8_t* codes, int64_t ldc, uint8_t* sf, int64_t ldsf,
