@@ -398,14 +398,15 @@ def _row_stride(t, what):
     return step if rows > 1 else cols  # a single row's pitch is never stepped over
 
 
-def _warn_no_gradient(level, a, b=None):
-    if torch.is_grad_enabled() and (a.requires_grad or (b is not None and b.requires_grad)):
+def _warn_no_gradient(level):
+    if torch.is_grad_enabled():
         warnings.warn("the result carries no gradient for its inputs: those of the grouped products are "
                       "beam_moe_grouped_gemm_dgrad and beam_moe_grouped_gemm_wgrad", stacklevel=level)
 
 
 def _grouped(offsets, a, b):
-    _warn_no_gradient(4, a, b)
+    if a.requires_grad or b.requires_grad:
+        _warn_no_gradient(4)
     kind = a.dtype
     if (kind is not torch.bfloat16 and kind is not torch.float16) or b.dtype is not kind:
         raise ValueError("the operands have to be both BF16 or both FP16")
@@ -521,7 +522,11 @@ def _fp4_matrix(codes, sf, fmt, what):
 def _tensor_scale(alpha, fmt, what):
     if alpha is None or fmt == "mxfp4":
         return None
-    if getattr(alpha, "dtype", None) is not torch.float32 or alpha.numel() != 1:
+    try:
+        good = alpha.dtype is torch.float32 and alpha.numel() == 1
+    except AttributeError:  # a plain number
+        good = False
+    if not good:
         raise ValueError(f"{what} has to be one FP32 value on the device")
     return alpha
 
@@ -534,12 +539,13 @@ def beam_moe_quantize_fp4(src, fmt, alpha=None, stream=None):
     alpha is the tensor scale, a float; None takes the largest finite value / 2688, found on
     the device.  The alpha returned is an FP32 tensor [1] (None for MXFP4)."""
     form = _fp4_format(fmt)
-    _warn_no_gradient(3, src)
+    if src.requires_grad:
+        _warn_no_gradient(3)
     kind = TYPES.get(src.dtype)
     if kind is None:
         raise ValueError("src has to be BF16, FP16 or FP32")
     # as the library gets it: a positive number that rounds to 0 would ask it to find the scale
-    if alpha is not None and not 0.0 < ctypes.c_float(alpha).value < float("inf"):
+    if alpha is not None and not (1e-44 < alpha < 3.4e38 or 0.0 < ctypes.c_float(alpha).value < float("inf")):
         raise ValueError("alpha has to be a positive finite FP32 number")
     ld = _row_stride(src, "src")
     rows, cols = src.shape
